@@ -1,0 +1,419 @@
+// ssd_linear.cu -- linear attention with a decay per head on CUDA cores: the scan for any
+// supported shape and type, the state pass between segments, the sum over shared heads' gradients
+// and the decode step. The tensor-core scan is ssd_linear_tc.cu.
+#include "../../include/ssd_mixer.h"
+#include "ssd_common.cuh"
+#include "ssd_linear.h"
+#include "ssd_profile.h"
+
+namespace ssd {
+namespace {
+
+// ---------------------------------------------------------------------------- the scan
+// Token by token: the recurrence needs 4 DK DV flops a token, fewer than any chunked form, and
+// keeps fp32 throughout, so fp32 activations and the shapes without a tensor-core variant use it.
+// A CTA owns one segment of one (sequence, head) row; a warp owns 8 state rows (16 when DK = 16)
+// in registers, its lanes along DK. Tokens come in tiles of 16 through shared memory, the next
+// tile's loads in flight while the present one is used. The products S q are summed over the lanes
+// by a butterfly that halves the values with each of its first three steps (9 shuffles for 8 rows).
+constexpr int kTile = 16;
+
+template <int DK>
+struct SimtShape {
+    static constexpr int kCols = DK >= 32 ? DK / 32 : 1;      // state columns per lane
+    static constexpr int kLanes = DK / kCols;                 // lanes per state row (32, or 16)
+    static constexpr int kRows = 8;                           // state rows per lane
+    static constexpr int kWarpRows = kRows * (32 / kLanes);
+};
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV / SimtShape<DK>::kWarpRows : 1))
+    linear_scan_kernel(const LinearCall c, const LinearScan s, bool state_only)
+{
+    using Sh = SimtShape<DK>;
+    constexpr int kWarps = DV / Sh::kWarpRows > 0 ? DV / Sh::kWarpRows : 1;
+    constexpr int kThr = 32 * kWarps;
+    constexpr int kVec = Act<T>::kVec;
+    constexpr int kRowVecs = (2 * DK + DV) / kVec;            // 16-byte vectors of one token's k, q, v
+    constexpr int kTileVecs = kTile * kRowVecs;
+    constexpr int kPer = (kTileVecs + kThr - 1) / kThr;
+    __shared__ __align__(16) T s_in[kTile][2 * DK + DV];      // k, then q, then v
+    __shared__ __align__(16) float s_o[kTile][DV];
+
+    const int h = blockIdx.x % c.H;
+    const int64_t item = blockIdx.x / c.H;
+    LinearItem it;
+    if (!linear_item(c, item, &it)) return;
+    // segments in scan order; the state-only pass covers all but the last of a row
+    const bool last = s.reverse ? it.seg == 0 : it.seg == it.nseg - 1;
+    if (state_only && last) return;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int sub = lane / Sh::kLanes, l = lane % Sh::kLanes;
+    const int d0 = warp * Sh::kWarpRows + sub * Sh::kRows;    // this lane's first state row
+    const int e0 = l * Sh::kCols;                             // and first column
+    const LinearDecay decay(linear_log_decay(c.log_decay, h));
+    const int64_t hs = (int64_t)DK * DV;
+
+    float S[Sh::kRows][Sh::kCols];
+#pragma unroll
+    for (int r = 0; r < Sh::kRows; ++r)
+#pragma unroll
+        for (int e = 0; e < Sh::kCols; ++e) S[r][e] = 0.0f;
+    if (!state_only) {
+        if (it.nseg > 1) {   // never the slot itself: the row's last segment may be rewriting it
+            const float* p = s.seg_states + (item * c.H + h) * hs;
+#pragma unroll
+            for (int r = 0; r < Sh::kRows; ++r)
+#pragma unroll
+                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = p[(d0 + r) * DK + e0 + e];
+        } else if (linear_has_init(c, s, it.seq)) {
+            const float* p = s.init + (it.slot * c.H + h) * hs;
+#pragma unroll
+            for (int r = 0; r < Sh::kRows; ++r)
+#pragma unroll
+                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = p[(d0 + r) * s.init_rs + (e0 + e) * s.init_cs];
+        }
+    }
+
+    const T* kp = (const T*)s.k + (int64_t)(h / s.k_share) * DK;
+    const T* qp = (const T*)s.q + (int64_t)(h / s.q_share) * DK;
+    const T* vp = (const T*)s.v + (int64_t)(h / s.v_share) * DV;
+    const int ntiles = (int)((it.n + kTile - 1) / kTile);
+    uint4 next[kPer];
+    // tile i of the segment in scan order: tokens kTile * ti ..
+    auto tile_of = [&](int i) { return s.reverse ? ntiles - 1 - i : i; };
+    auto fetch = [&](int i) {
+        const int64_t t0 = (int64_t)tile_of(i) * kTile;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int id = tid + x * kThr;
+            const int tt = id / kRowVecs, w = (id % kRowVecs) * kVec;
+            next[x] = make_uint4(0, 0, 0, 0);
+            if (id < kTileVecs && t0 + tt < it.n) {
+                const int64_t row = it.row0 + t0 + tt;
+                const T* p = w < DK ? kp + row * s.k_ld + w
+                                    : w < 2 * DK ? qp + row * s.q_ld + (w - DK) : vp + row * s.v_ld + (w - 2 * DK);
+                next[x] = *reinterpret_cast<const uint4*>(p);
+            }
+        }
+    };
+    if (ntiles > 0) fetch(0);
+    bool fresh = s.reverse;      // the first backward step has no decay
+    for (int i = 0; i < ntiles; ++i) {
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int id = tid + x * kThr;
+            if (id < kTileVecs) *reinterpret_cast<uint4*>(&s_in[id / kRowVecs][(id % kRowVecs) * kVec]) = next[x];
+        }
+        __syncthreads();
+        if (i + 1 < ntiles) fetch(i + 1);
+        const int64_t t0 = (int64_t)tile_of(i) * kTile;
+        const int nt = it.n - t0 < kTile ? (int)(it.n - t0) : kTile;
+        for (int x = 0; x < nt; ++x) {
+            const int tt = s.reverse ? nt - 1 - x : x;
+            float kk[Sh::kCols], v[Sh::kRows];
+#pragma unroll
+            for (int e = 0; e < Sh::kCols; ++e) kk[e] = ld_f(&s_in[tt][e0 + e]);
+#pragma unroll
+            for (int r = 0; r < Sh::kRows; ++r) v[r] = s.u_scale * ld_f(&s_in[tt][2 * DK + d0 + r]);
+            if (fresh || decay.slow) {     // two versions, two operations an element each
+                const float f = fresh ? 0.0f : decay.f;
+#pragma unroll
+                for (int r = 0; r < Sh::kRows; ++r)
+#pragma unroll
+                    for (int e = 0; e < Sh::kCols; ++e) S[r][e] = fmaf(f, S[r][e], fmaf(v[r], kk[e], S[r][e]));
+            } else {
+#pragma unroll
+                for (int r = 0; r < Sh::kRows; ++r)
+#pragma unroll
+                    for (int e = 0; e < Sh::kCols; ++e) S[r][e] = fmaf(decay.f, S[r][e], v[r] * kk[e]);
+            }
+            fresh = false;
+            if (!state_only) {
+                float o[Sh::kRows];
+#pragma unroll
+                for (int r = 0; r < Sh::kRows; ++r) o[r] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < Sh::kCols; ++e) {
+                    const float qq = ld_f(&s_in[tt][DK + e0 + e]);
+#pragma unroll
+                    for (int r = 0; r < Sh::kRows; ++r) o[r] = fmaf(S[r][e], qq, o[r]);
+                }
+                // lanes with the offset's bit set keep the upper half of the rows, the others the lower
+                int row = 0;
+#pragma unroll
+                for (int half = Sh::kRows / 2, off = Sh::kLanes / 2; half > 0; half >>= 1, off >>= 1) {
+                    const bool up = (l & off) != 0;
+#pragma unroll
+                    for (int r = 0; r < half; ++r) {
+                        const float give = up ? o[r] : o[r + half];
+                        const float keep = up ? o[r + half] : o[r];
+                        o[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                    row += up ? half : 0;
+                }
+#pragma unroll
+                for (int off = Sh::kLanes / 16; off > 0; off >>= 1) o[0] += __shfl_xor_sync(0xffffffffu, o[0], off);
+                if ((l & (Sh::kLanes / 8 - 1)) == 0) s_o[tt][d0 + row] = s.out_scale * o[0];
+            }
+        }
+        if (!state_only) {
+            __syncthreads();
+            for (int id = tid; id < nt * DV; id += kThr) {
+                const int tt = id / DV, d = id % DV;
+                const int64_t at = (it.row0 + t0 + tt) * s.o_ld + (int64_t)h * DV + d;
+                if (s.o_f32) ((float*)s.o)[at] = s_o[tt][d];
+                else ((T*)s.o)[at] = Act<T>::from_f(s_o[tt][d]);
+            }
+        }
+    }
+    if (s.reverse && it.n > 0) {
+#pragma unroll
+        for (int r = 0; r < Sh::kRows; ++r)
+#pragma unroll
+            for (int e = 0; e < Sh::kCols; ++e) S[r][e] = decay.step(S[r][e], 0.0f);
+    }
+    float* out = nullptr;
+    if (state_only) out = s.seg_states + (item * c.H + h) * hs;
+    else if (last && s.final_state) out = s.final_state + (it.slot * c.H + h) * hs;
+    if (out) {
+#pragma unroll
+        for (int r = 0; r < Sh::kRows; ++r)
+#pragma unroll
+            for (int e = 0; e < Sh::kCols; ++e) out[(d0 + r) * DK + e0 + e] = S[r][e];
+    }
+}
+
+template <typename T, int DK, int DV>
+void launch_scan_shape(const LinearCall& c, const LinearScan& s, bool state_only, cudaStream_t st)
+{
+    constexpr int kWarps = DV / SimtShape<DK>::kWarpRows > 0 ? DV / SimtShape<DK>::kWarpRows : 1;
+    LaunchScope ls(state_only ? "linear_states" : "linear_scan", st);
+    linear_scan_kernel<T, DK, DV><<<(unsigned)(c.items * c.H), 32 * kWarps, 0, st>>>(c, s, state_only);
+}
+template <typename T, int DK>
+void launch_scan_dv(const LinearCall& c, const LinearScan& s, bool so, cudaStream_t st)
+{
+    switch (s.DV) {
+    case 16: return launch_scan_shape<T, DK, 16>(c, s, so, st);
+    case 32: return launch_scan_shape<T, DK, 32>(c, s, so, st);
+    case 64: return launch_scan_shape<T, DK, 64>(c, s, so, st);
+    default: return launch_scan_shape<T, DK, 128>(c, s, so, st);
+    }
+}
+template <typename T>
+void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, cudaStream_t st)
+{
+    switch (s.DK) {
+    case 16: return launch_scan_dv<T, 16>(c, s, so, st);
+    case 32: return launch_scan_dv<T, 32>(c, s, so, st);
+    case 64: return launch_scan_dv<T, 64>(c, s, so, st);
+    default: return launch_scan_dv<T, 128>(c, s, so, st);
+    }
+}
+
+// ------------------------------------------------------------- states between segments
+// Rows of one segment are left alone. Before: seg_states[t] holds segment t's own state from a zero
+// start (the last segment of the scan has none). After: the state entering segment t.
+__global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, const LinearScan s)
+{
+    const int h = blockIdx.y;
+    const int64_t seq = blockIdx.z;
+    const int hs = s.DK * s.DV;
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    int64_t item0 = seq * c.nseg;
+    if (c.cu_seqlens) {
+        int64_t start = c.cu_seqlens[seq];
+        start = start < 0 ? 0 : (start > c.T ? c.T : start);
+        item0 = seq + start / c.seg_tokens;
+    }
+    LinearItem it;
+    if (i >= hs || !linear_item(c, item0, &it) || it.nseg < 2) return;
+    const int d = i / s.DK, e = i - d * s.DK;
+    const float g = linear_log_decay(c.log_decay, h);
+    float S = linear_has_init(c, s, seq) ? s.init[(it.slot * c.H + h) * (int64_t)hs + (int64_t)d * s.init_rs + (int64_t)e * s.init_cs] : 0.0f;
+    for (int64_t k = 0; k < it.nseg; ++k) {
+        const int64_t t = s.reverse ? it.nseg - 1 - k : k;
+        LinearItem seg;
+        if (!linear_item(c, item0 + t, &seg)) return;
+        float* p = s.seg_states + ((item0 + t) * c.H + h) * (int64_t)hs + i;
+        const float own = k + 1 < it.nseg ? *p : 0.0f;
+        *p = S;
+        S = LinearDecay(g * (float)seg.n).step(S, own);
+    }
+}
+
+// ------------------------------------------------------------- gradients of shared heads
+// out[row][g][d] = sum of the r heads of group g, in fp32, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_group_sum_kernel(const float* __restrict__ in, T* __restrict__ out, int64_t ld,
+                                                               int64_t n, int G, int r, int D)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const int64_t w = (int64_t)G * D, row = i / w;
+    const int col = (int)(i - row * w), g = col / D, d = col - g * D;
+    const float* p = in + (row * G + g) * (int64_t)r * D + d;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < r; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)k * D);
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    }
+    T* o = out + row * ld + col;
+    o[0] = Act<T>::from_f(a.x); o[1] = Act<T>::from_f(a.y); o[2] = Act<T>::from_f(a.z); o[3] = Act<T>::from_f(a.w);
+}
+
+// ---------------------------------------------------------------------------- decode
+// One token a sequence, states in place: the fp32 state is read once and written once, which is
+// nearly all of the bytes. Lanes along DK (a float4 each), kRif state rows in flight per lane, so a
+// CTA's whole part of the state is on its way before the first product.
+constexpr int kDecodeThreads = 128, kRif = 8;
+
+struct LinearDecode {
+    const void *q, *k, *v;
+    int64_t q_ld, k_ld, v_ld, o_ld;
+    const float* log_decay;
+    float* state;
+    const int32_t* slot_idx;
+    int64_t nslots;
+    void* o;
+    int H, share, DV, parts;
+    float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p)
+{
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+}
+
+template <typename T, int DK>
+__global__ void __launch_bounds__(kDecodeThreads) linear_decode_kernel(const LinearDecode p)
+{
+    constexpr int kLanes = DK / 4, kRows = kDecodeThreads / kLanes;   // rows of one pass of the CTA
+    const int64_t seq = blockIdx.y;
+    const int h = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+    const int64_t slot = p.slot_idx ? (int64_t)p.slot_idx[seq] : seq;
+    if (slot < 0 || slot >= p.nslots) return;
+    const int l = threadIdx.x % kLanes, r0 = part * kRows * kRif + threadIdx.x / kLanes;
+    float4* S = reinterpret_cast<float4*>(p.state + ((slot * p.H + h) * p.DV) * DK) + l;
+    float4 s[kRif];
+#pragma unroll
+    for (int i = 0; i < kRif; ++i) {
+        const int r = r0 + i * kRows;
+        if (r < p.DV) s[i] = S[(int64_t)r * kLanes];
+    }
+    const LinearDecay decay(linear_log_decay(p.log_decay, h));
+    const float4 k = load4((const T*)p.k + seq * p.k_ld + (int64_t)(h / p.share) * DK + 4 * l);
+    const float4 q = load4((const T*)p.q + seq * p.q_ld + (int64_t)h * DK + 4 * l);
+    const T* vp = (const T*)p.v + seq * p.v_ld + (int64_t)(h / p.share) * p.DV;
+    T* op = (T*)p.o + seq * p.o_ld + (int64_t)h * p.DV;
+#pragma unroll
+    for (int i = 0; i < kRif; ++i) {
+        const int r = r0 + i * kRows;
+        const bool in = r < p.DV;
+        float o = 0.0f;
+        if (in) {
+            const float v = ld_f(vp + r);
+            float4 n;
+            n.x = decay.step(s[i].x, v * k.x);
+            n.y = decay.step(s[i].y, v * k.y);
+            n.z = decay.step(s[i].z, v * k.z);
+            n.w = decay.step(s[i].w, v * k.w);
+            S[(int64_t)r * kLanes] = n;
+            o = n.x * q.x + n.y * q.y + n.z * q.z + n.w * q.w;
+        }
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
+        if (in && l == 0) op[r] = Act<T>::from_f(p.scale * o);
+    }
+}
+
+template <typename T>
+void launch_decode(const LinearDecode& p, int DK, int64_t b, cudaStream_t st)
+{
+    LaunchScope ls("linear_decode", st);
+    const dim3 grid((unsigned)(p.H * p.parts), (unsigned)b);
+    switch (DK) {
+    case 16: linear_decode_kernel<T, 16><<<grid, kDecodeThreads, 0, st>>>(p); break;
+    case 32: linear_decode_kernel<T, 32><<<grid, kDecodeThreads, 0, st>>>(p); break;
+    case 64: linear_decode_kernel<T, 64><<<grid, kDecodeThreads, 0, st>>>(p); break;
+    default: linear_decode_kernel<T, 128><<<grid, kDecodeThreads, 0, st>>>(p); break;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStream_t st)
+{
+    if (c.items == 0) return cudaSuccess;
+    const auto run = [&](bool state_only) {
+        if (c.act == SSD_BF16) launch_scan_dk<__nv_bfloat16>(c, s, state_only, st);
+        else launch_scan_dk<float>(c, s, state_only, st);
+        return cudaGetLastError();
+    };
+    if (c.split) {
+        cudaError_t e = run(true);
+        if (e != cudaSuccess) return e;
+        e = launch_linear_pass(c, s, st);
+        if (e != cudaSuccess) return e;
+    }
+    return run(false);
+}
+
+cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st)
+{
+    LaunchScope ls("linear_pass", st);
+    linear_pass_kernel<<<dim3((unsigned)((s.DK * s.DV + 255) / 256), (unsigned)c.H, (unsigned)c.b), 256, 0, st>>>(c, s);
+    return cudaGetLastError();
+}
+
+int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms)
+{
+    // Enough segments for every SM to have work, none under 128 tokens.
+    const int64_t want = (int64_t)sms * (tc ? 1 : 2);
+    const int64_t rows = b * H * nscans;
+    const int64_t len = packed ? T : L;
+    if (rows >= want || len <= 128) return len > 0 ? ((len + 127) / 128) * 128 + 128 : 128;
+    const int64_t per = packed ? (T * H * nscans + want - 1) / want : L / ((want + rows - 1) / rows);
+    const int64_t blocks = (per + 127) / 128;
+    return (blocks > 0 ? blocks : 1) * 128;
+}
+
+cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,
+                                    cudaStream_t st)
+{
+    const int64_t n = rows * G * (int64_t)D;
+    if (n == 0) return cudaSuccess;
+    LaunchScope ls("linear_group_sum", st);
+    const unsigned grid = (unsigned)((n / 4 + 255) / 256);
+    if (act == SSD_BF16) linear_group_sum_kernel<<<grid, 256, 0, st>>>(in, (__nv_bfloat16*)out, ld, n, G, r, D);
+    else linear_group_sum_kernel<<<grid, 256, 0, st>>>(in, (float*)out, ld, n, G, r, D);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_decode(int64_t b, int H, int share, int DK, int DV, float scale, int act, const void* q,
+                                 int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                                 const float* log_decay, float* state, int64_t nslots, const int32_t* slot_idx, void* o,
+                                 int64_t o_ld, cudaStream_t st)
+{
+    LinearDecode p{q, k, v, q_ld, k_ld, v_ld, o_ld, log_decay, state, slot_idx, nslots, o, H, share, DV, 0, scale};
+    const int rows = kDecodeThreads / (DK / 4) * kRif;
+    p.parts = (DV + rows - 1) / rows;
+    if (act == SSD_BF16) launch_decode<__nv_bfloat16>(p, DK, b, st);
+    else launch_decode<float>(p, DK, b, st);
+    return cudaGetLastError();
+}
+
+bool linear_tc_supported(const LinearScan&, int) { return false; }
+cudaError_t launch_linear_tc(const LinearCall&, const LinearScan*, int, cudaStream_t) { return cudaErrorNotSupported; }
+
+}  // namespace ssd

@@ -16,6 +16,12 @@ The entry points keep the C names:
                      <gradients>, workspace, stream=None)
 plus :func:`prefill` / :func:`decode_step` / :func:`backward`, which allocate the outputs
 and workspace with torch and call the entry points above.
+
+Linear attention with a decay per head (:class:`LinearDims`, :func:`linear_prefill`,
+:func:`linear_prefill_varlen`, :func:`linear_decode_step`, :func:`linear_backward`) and the
+grouped layer norm (:func:`layer_norm`, :func:`layer_norm_backward`) check every tensor's type,
+shape and device, run on the device of their inputs whichever is current, and allocate what is
+not given. Unless ``stream`` is given, they run on that device's current stream.
 """
 from __future__ import annotations
 
@@ -41,7 +47,11 @@ SYMBOLS = ("ssd_mixer_prefill_workspace_size", "ssd_mixer_prefill", "ssd_mixer_d
            "ssd_mixer_backward_workspace_size", "ssd_mixer_backward", "ssd_mixer_selftest_wait",
            "ssd_mixer_prefill_static_status", "ssd_mixer_prefill_path", "ssd_mixer_prefill_plan",
            "ssd_mixer_prefill_stage_offsets",
-           "ssd_mixer_projection", "ssd_mixer_layer_workspace_size", "ssd_mixer_layer_prefill")
+           "ssd_mixer_projection", "ssd_mixer_layer_workspace_size", "ssd_mixer_layer_prefill",
+           "ssd_mixer_linear_prefill_workspace_size", "ssd_mixer_linear_prefill",
+           "ssd_mixer_linear_prefill_varlen_workspace_size", "ssd_mixer_linear_prefill_varlen",
+           "ssd_mixer_linear_decode_step", "ssd_mixer_linear_backward_workspace_size", "ssd_mixer_linear_backward",
+           "ssd_mixer_layer_norm", "ssd_mixer_layer_norm_backward_workspace_size", "ssd_mixer_layer_norm_backward")
 SSD_PATH_NONE, SSD_PATH_CUDA_CORES, SSD_PATH_TENSOR_CORES = range(3)
 
 
@@ -89,6 +99,36 @@ class Dims:
                       self.dstate, self.dconv, self.chunk, self.eps,
                       SSD_BF16 if self.act == "bf16" else SSD_F32)
 
+
+class _CLinearDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int32),
+                ("ngroups", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("act", ctypes.c_int32)]
+
+
+@dataclass(frozen=True)
+class LinearDims:
+    """Sizes of a linear-attention call: batch rows (or packed sequences) of seqlen tokens (packed
+    call: token rows in all; decode: 1), nheads heads, ngroups heads of k and v."""
+    batch: int
+    seqlen: int
+    nheads: int
+    ngroups: int
+    dk: int
+    dv: int
+    scale: float = 1.0
+    act: str = "bf16"
+
+    @property
+    def torch_dtype(self):
+        return _ACT_DTYPES[self.act]
+
+    def c(self) -> _CLinearDims:
+        return _CLinearDims(self.batch, self.seqlen, self.nheads, self.ngroups, self.dk, self.dv, self.scale,
+                            SSD_BF16 if self.act == "bf16" else SSD_F32)
+
+
+_ACT_DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 _lib = None
 
@@ -151,6 +191,25 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_mixer_backward.argtypes = ([ctypes.POINTER(_CDims)] + [P, I64] * 5 + [FP] * 6 + [FP, P] +
                                        [P, I64, FP, FP] + [P, I64] * 5 + [FP] * 8 + [P, ctypes.c_size_t, V])
     lib.ssd_mixer_backward.restype = ctypes.c_int
+    LD, I32, SZ = ctypes.POINTER(_CLinearDims), ctypes.c_int32, ctypes.c_size_t
+    for n in ("prefill", "prefill_varlen", "backward"):
+        f = getattr(lib, f"ssd_mixer_linear_{n}_workspace_size")
+        f.argtypes, f.restype = [LD], SZ
+    lib.ssd_mixer_linear_prefill.argtypes = [LD] + [P, I64] * 3 + [FP, FP, P, I64, FP, P, SZ, V]
+    lib.ssd_mixer_linear_prefill.restype = ctypes.c_int
+    lib.ssd_mixer_linear_prefill_varlen.argtypes = [LD, P, P, P] + [P, I64] * 3 + [FP, FP, I64, P, I64, P, SZ, V]
+    lib.ssd_mixer_linear_prefill_varlen.restype = ctypes.c_int
+    lib.ssd_mixer_linear_decode_step.argtypes = [LD] + [P, I64] * 3 + [FP, FP, I64, P, P, I64, V]
+    lib.ssd_mixer_linear_decode_step.restype = ctypes.c_int
+    lib.ssd_mixer_linear_backward.argtypes = ([LD] + [P, I64] * 3 + [FP, FP, P, I64, FP] + [P, I64] * 3 +
+                                              [FP, P, SZ, V])
+    lib.ssd_mixer_linear_backward.restype = ctypes.c_int
+    lib.ssd_mixer_layer_norm.argtypes = [I64, I32, I32, ctypes.c_float, I32, P, I64, FP, FP, P, I64, FP, FP, V]
+    lib.ssd_mixer_layer_norm.restype = ctypes.c_int
+    lib.ssd_mixer_layer_norm_backward_workspace_size.argtypes = [I64, I32, I32, I32]
+    lib.ssd_mixer_layer_norm_backward_workspace_size.restype = SZ
+    lib.ssd_mixer_layer_norm_backward.argtypes = [I64, I32, I32, I32, P, I64, P, I64, FP, FP, FP, P, I64, FP, FP, P, SZ, V]
+    lib.ssd_mixer_layer_norm_backward.restype = ctypes.c_int
     lib.ssd_mixer_selftest_wait.argtypes = [P, ctypes.c_longlong, ctypes.c_int, V]
     lib.ssd_mixer_selftest_wait.restype = ctypes.c_int
     lib.ssd_mixer_workspace_status.argtypes = [P, V]
@@ -533,3 +592,286 @@ def decode_step(dims: Dims, x, z, B, C, dt, A, D, conv_w, conv_b, dt_bias, norm_
     ssd_mixer_decode_step(dims, x, z, B, C, dt, A, D, conv_w, conv_b, dt_bias, norm_w,
                           ssm_state, conv_state, slot_idx, y, stream)
     return y
+
+
+# ------------------------------------------------------- linear attention and layer norm
+def _rows_on(t, name: str, rows: int, width: int, dtype, dev):
+    """Pointer and row stride of `rows` evenly strided rows of `width` unit-stride elements, of the
+    given type and on the given device. Dimensions of size 1 set no stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+    shape = t.shape
+    if t.dim() < 1 or shape[-1] != width or t.numel() != rows * width:
+        raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(shape)}")
+    if rows == 0:
+        return t.data_ptr(), width
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: last dim must have unit stride")
+    ld, expect = width, None
+    for d in range(t.dim() - 2, -1, -1):
+        if shape[d] == 1:
+            continue
+        if expect is None:
+            ld = t.stride(d)
+            expect = ld * shape[d]
+        elif t.stride(d) != expect:
+            raise ValueError(f"{name}: rows must be evenly strided")
+        else:
+            expect *= shape[d]
+    return t.data_ptr(), ld
+
+
+def _whole(t, name: str, shape, dtype, dev):
+    """Pointer of a contiguous tensor of exactly this shape, type and device (None: NULL)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+class _On:
+    """Makes the tensors' device current and, where a stream is given, that stream too (so that what
+    the call allocates belongs to it). ``.ptr`` is the stream's handle."""
+    __slots__ = ("dev", "stream", "ctx", "ptr")
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.ctx = dev, stream, []
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            c = torch.cuda.device(self.dev)
+            c.__enter__()
+            self.ctx.append(c)
+        if self.stream is not None:
+            s = self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+                _stream(self.stream), device=self.dev)
+            if s.device != self.dev:
+                self.__exit__(None, None, None)
+                raise ValueError(f"the stream is on {s.device}, the tensors on {self.dev}")
+            c = torch.cuda.stream(s)
+            c.__enter__()
+            self.ctx.append(c)
+            self.ptr = s.cuda_stream
+        else:
+            self.ptr = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        while self.ctx:
+            self.ctx.pop().__exit__(*exc)
+        return False
+
+
+def _linear_dims(dims: LinearDims) -> _CLinearDims:
+    if dims.act not in _ACT_DTYPES:
+        raise ValueError(f"act: expected one of {sorted(_ACT_DTYPES)}, got {dims.act!r}")
+    return dims.c()
+
+
+def _linear_qkv(dims: LinearDims, rows: int, q, k, v, dev):
+    a, H, G = dims.torch_dtype, dims.nheads, dims.ngroups
+    return (*_rows_on(q, "q", rows, H * dims.dk, a, dev), *_rows_on(k, "k", rows, G * dims.dk, a, dev),
+            *_rows_on(v, "v", rows, G * dims.dv, a, dev))
+
+
+def _workspace(ws, size: int, what: str, dev):
+    """The given workspace's (or a new one's) pointer, bytes and tensor."""
+    if ws is None:
+        if size == 0:
+            raise SsdError(SSD_ERR_UNSUPPORTED, f"{what}: invalid or unsupported dims")
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def ssd_mixer_linear_prefill_workspace_size(dims: LinearDims) -> int:
+    return int(load_library().ssd_mixer_linear_prefill_workspace_size(ctypes.byref(_linear_dims(dims))))
+
+
+def ssd_mixer_linear_prefill_varlen_workspace_size(dims: LinearDims) -> int:
+    return int(load_library().ssd_mixer_linear_prefill_varlen_workspace_size(ctypes.byref(_linear_dims(dims))))
+
+
+def ssd_mixer_linear_backward_workspace_size(dims: LinearDims) -> int:
+    return int(load_library().ssd_mixer_linear_backward_workspace_size(ctypes.byref(_linear_dims(dims))))
+
+
+def linear_prefill(dims: LinearDims, q, k, v, log_decay, init_state=None, workspace=None, out=None, stream=None):
+    """Linear attention over b rows of L tokens (ssd_mixer_linear_prefill): q [b, L, H * dk], k
+    [b, L, G * dk], v [b, L, G * dv], log_decay [H] fp32, init_state [b, H, dv, dk] fp32 or None.
+    Returns (o [b, L, H * dv], final_state); ``out`` gives both tensors."""
+    dev = _device_of(q, "q")
+    cd = _linear_dims(dims)
+    b, L, H = dims.batch, dims.seqlen, dims.nheads
+    rows = _linear_qkv(dims, b * L, q, k, v, dev)
+    sshape = (b, H, dims.dv, dims.dk)
+    pd = _whole(log_decay, "log_decay", (H,), torch.float32, dev)
+    pi = _whole(init_state, "init_state", sshape, torch.float32, dev)
+    lib = load_library()
+    with _On(dev, stream) as on:
+        if out is None:
+            o = torch.empty(b, L, H * dims.dv, dtype=dims.torch_dtype, device=dev)
+            fs = torch.empty(sshape, dtype=torch.float32, device=dev)
+        else:
+            o, fs = out
+        po = _rows_on(o, "o", b * L, H * dims.dv, dims.torch_dtype, dev)
+        pf = _whole(fs, "final_state", sshape, torch.float32, dev)
+        pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
+                                lib.ssd_mixer_linear_prefill_workspace_size(ctypes.byref(cd)), "linear_prefill", dev)
+        st = lib.ssd_mixer_linear_prefill(ctypes.byref(cd), *rows, pd, pi, *po, pf, pw, nw, on.ptr)
+    _check(st, "ssd_mixer_linear_prefill")
+    return o, fs
+
+
+def linear_prefill_varlen(dims: LinearDims, cu_seqlens, slot_idx, has_init, q, k, v, log_decay, state, workspace=None,
+                          o=None, stream=None):
+    """Linear attention over packed sequences on state slots (ssd_mixer_linear_prefill_varlen): q
+    [T, H * dk] ..., state [nslots, H, dv, dk] fp32 updated in place; cu_seqlens int32 [b + 1],
+    slot_idx int32 [b] or None, has_init uint8 [b] or None. Returns o [T, H * dv]."""
+    dev = _device_of(q, "q")
+    cd = _linear_dims(dims)
+    b, T, H = dims.batch, dims.seqlen, dims.nheads
+    rows = _linear_qkv(dims, T, q, k, v, dev)
+    pcu = _whole(cu_seqlens, "cu_seqlens", (b + 1,), torch.int32, dev)
+    psl = _whole(slot_idx, "slot_idx", (b,), torch.int32, dev)
+    phi = _whole(has_init, "has_init", (b,), torch.uint8, dev)
+    pd = _whole(log_decay, "log_decay", (H,), torch.float32, dev)
+    nslots = int(state.shape[0]) if isinstance(state, torch.Tensor) and state.dim() else 0
+    ps = _whole(state, "state", (nslots, H, dims.dv, dims.dk), torch.float32, dev)
+    lib = load_library()
+    with _On(dev, stream) as on:
+        if o is None:
+            o = torch.empty(T, H * dims.dv, dtype=dims.torch_dtype, device=dev)
+        po = _rows_on(o, "o", T, H * dims.dv, dims.torch_dtype, dev)
+        pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
+                                lib.ssd_mixer_linear_prefill_varlen_workspace_size(ctypes.byref(cd)),
+                                "linear_prefill_varlen", dev)
+        st = lib.ssd_mixer_linear_prefill_varlen(ctypes.byref(cd), pcu, psl, phi, *rows, pd, ps, nslots, *po, pw, nw,
+                                                 on.ptr)
+    _check(st, "ssd_mixer_linear_prefill_varlen")
+    return o
+
+
+def linear_decode_step(dims: LinearDims, q, k, v, log_decay, state, slot_idx=None, o=None, stream=None):
+    """One token of each of b sequences (ssd_mixer_linear_decode_step): q [b, H * dk] ..., state
+    [nslots, H, dv, dk] fp32 updated in place. Returns o [b, H * dv]."""
+    dev = _device_of(q, "q")
+    cd = _linear_dims(dims)
+    b, H = dims.batch, dims.nheads
+    rows = _linear_qkv(dims, b, q, k, v, dev)
+    psl = _whole(slot_idx, "slot_idx", (b,), torch.int32, dev)
+    pd = _whole(log_decay, "log_decay", (H,), torch.float32, dev)
+    nslots = int(state.shape[0]) if isinstance(state, torch.Tensor) and state.dim() else 0
+    ps = _whole(state, "state", (nslots, H, dims.dv, dims.dk), torch.float32, dev)
+    with _On(dev, stream) as on:
+        if o is None:
+            o = torch.empty(b, H * dims.dv, dtype=dims.torch_dtype, device=dev)
+        po = _rows_on(o, "o", b, H * dims.dv, dims.torch_dtype, dev)
+        st = load_library().ssd_mixer_linear_decode_step(ctypes.byref(cd), *rows, pd, ps, nslots, psl, *po, on.ptr)
+    _check(st, "ssd_mixer_linear_decode_step")
+    return o
+
+
+def linear_backward(dims: LinearDims, q, k, v, log_decay, do, init_state=None, dfinal_state=None, workspace=None,
+                    stream=None) -> dict:
+    """Gradients of :func:`linear_prefill` (ssd_mixer_linear_backward) from do [b, L, H * dv] and,
+    optionally, that of the final state. Returns {"q", "k", "v", "init_state"}."""
+    dev = _device_of(q, "q")
+    cd = _linear_dims(dims)
+    b, L, H, G, a = dims.batch, dims.seqlen, dims.nheads, dims.ngroups, dims.torch_dtype
+    rows = _linear_qkv(dims, b * L, q, k, v, dev)
+    sshape = (b, H, dims.dv, dims.dk)
+    pd = _whole(log_decay, "log_decay", (H,), torch.float32, dev)
+    pi = _whole(init_state, "init_state", sshape, torch.float32, dev)
+    pdo = _rows_on(do, "do", b * L, H * dims.dv, a, dev)
+    pdf = _whole(dfinal_state, "dfinal_state", sshape, torch.float32, dev)
+    lib = load_library()
+    with _On(dev, stream) as on:
+        g = {"q": torch.empty(b, L, H * dims.dk, dtype=a, device=dev), "k": torch.empty(b, L, G * dims.dk, dtype=a, device=dev),
+             "v": torch.empty(b, L, G * dims.dv, dtype=a, device=dev),
+             "init_state": torch.empty(sshape, dtype=torch.float32, device=dev)}
+        outs = []
+        for n, w in (("q", H * dims.dk), ("k", G * dims.dk), ("v", G * dims.dv)):
+            outs += [g[n].data_ptr(), w]
+        pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
+                                lib.ssd_mixer_linear_backward_workspace_size(ctypes.byref(cd)), "linear_backward", dev)
+        st = lib.ssd_mixer_linear_backward(ctypes.byref(cd), *rows, pd, pi, *pdo, pdf, *outs, g["init_state"].data_ptr(),
+                                           pw, nw, on.ptr)
+    _check(st, "ssd_mixer_linear_backward")
+    return g
+
+
+def _norm_args(x, weight, groups: int):
+    dev = _device_of(x, "x")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x: expected fp32 or bf16, got {x.dtype}")
+    if x.dim() < 1 or groups <= 0 or x.shape[-1] == 0 or x.shape[-1] % groups:
+        raise ValueError(f"x: the last dim of {tuple(x.shape)} is not a multiple of groups = {groups}")
+    C = x.shape[-1]
+    rows = x.numel() // C
+    return dev, C, rows, C // groups, SSD_BF16 if x.dtype == torch.bfloat16 else SSD_F32, _rows_on(x, "x", rows, C, x.dtype, dev)
+
+
+def layer_norm(x, weight=None, bias=None, groups: int = 1, eps: float = 1e-5, out=None, stream=None):
+    """Layer norm over each of ``groups`` contiguous runs of x's last dim (ssd_mixer_layer_norm);
+    weight and bias [x.shape[-1]] fp32 or None. Returns (y, mean, rstd), the statistics fp32 of shape
+    [*x.shape[:-1], groups]; ``out`` gives y (which may be x)."""
+    dev, C, rows, width, act, px = _norm_args(x, weight, groups)
+    pw = _whole(weight, "weight", (C,), torch.float32, dev)
+    pb = _whole(bias, "bias", (C,), torch.float32, dev)
+    with _On(dev, stream) as on:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        py = _rows_on(y, "out", rows, C, x.dtype, dev)
+        stats = torch.empty((2, *x.shape[:-1], groups), dtype=torch.float32, device=dev)
+        pm = stats.data_ptr()
+        st = load_library().ssd_mixer_layer_norm(rows, groups, width, eps, act, *px, pw, pb, *py, pm,
+                                                 pm + 4 * rows * groups, on.ptr)
+    _check(st, "ssd_mixer_layer_norm")
+    return y, stats[0], stats[1]
+
+
+def ssd_mixer_layer_norm_backward_workspace_size(rows: int, groups: int, width: int, act: str) -> int:
+    return int(load_library().ssd_mixer_layer_norm_backward_workspace_size(rows, groups, width,
+                                                                          SSD_BF16 if act == "bf16" else SSD_F32))
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, groups: int = 1, workspace=None, stream=None):
+    """Gradients of :func:`layer_norm` (ssd_mixer_layer_norm_backward) from dy, x and the saved
+    statistics. Returns (dx, dweight, dbias), the parameters' in fp32."""
+    dev, C, rows, width, act, px = _norm_args(x, weight, groups)
+    pdy = _rows_on(dy, "dy", rows, C, x.dtype, dev)
+    pw = _whole(weight, "weight", (C,), torch.float32, dev)
+    sshape = (*x.shape[:-1], groups)
+    pm, pr = _whole(mean, "mean", sshape, torch.float32, dev), _whole(rstd, "rstd", sshape, torch.float32, dev)
+    lib = load_library()
+    with _On(dev, stream) as on:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dpar = torch.empty(2, C, dtype=torch.float32, device=dev)
+        pp = dpar.data_ptr()
+        pws, nws, ws = _workspace(workspace, 0 if workspace is not None else
+                                  lib.ssd_mixer_layer_norm_backward_workspace_size(rows, groups, width, act),
+                                  "layer_norm_backward", dev)
+        st = lib.ssd_mixer_layer_norm_backward(rows, groups, width, act, *pdy, *px, pw, pm, pr, dx.data_ptr(), C, pp,
+                                               pp + 4 * C, pws, nws, on.ptr)
+    _check(st, "ssd_mixer_layer_norm_backward")
+    return dx, dpar[0], dpar[1]

@@ -424,6 +424,119 @@ SSD_API ssd_status ssd_mixer_backward(const ssd_dims* dims,
                               void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* Linear attention with a decay per head: the scan of hybrid layers whose decay is a constant of
+ * the head (no counterpart in the pages, whose scan's decay follows from each token's dt). It has
+ * neither conv, gate nor norm; H heads, key dim dk, value dim dv, G heads of k and v (head h reads
+ * k and v head h / (H/G)). With l = exp(log_decay[h]):
+ *   S_t = l S_{t-1} + v_t (outer) k_t,   o_t = scale S_t q_t.
+ * The state S is fp32 [H][dv][dk], dk contiguous (the layout of the SSM state). log_decay [H] fp32,
+ * at most 0, is a constant: no gradient with respect to it is computed. -inf keeps the current
+ * token alone, 0 forgets nothing.
+ *
+ * Shared by the linear_* calls: row layouts as above, each row's heads side by side (q [..][H][dk],
+ * k [..][G][dk], v [..][G][dv], o [..][H][dv]), strides of at least that many elements; pointers
+ * 16-byte aligned with ld * elem_size a multiple of 16 bytes, otherwise SSD_ERR_UNSUPPORTED; o and
+ * the gradients must not overlap the inputs or one another. dk and dv: 16, 32, 64 or 128, in any
+ * pairing. Arithmetic is fp32; bf16 calls with dk and dv of 64 or 128 run their products on the
+ * tensor cores with fp32 accumulation, the decayed scores and the state's operand copy rounded to
+ * bf16, the state itself carried in fp32 and added to from products of bf16 pairs (hi + lo). */
+typedef struct ssd_linear_dims {
+    int64_t batch;    /* sequences */
+    int64_t seqlen;   /* tokens per row (packed call: token rows in all; decode: must be 1) */
+    int32_t nheads;   /* H */
+    int32_t ngroups;  /* G: divides H */
+    int32_t dk, dv;   /* 16, 32, 64 or 128 */
+    float scale;      /* factor of o, finite (often dk^-1/2) */
+    int32_t act;      /* ssd_dtype of q, k, v, o and their gradients */
+} ssd_linear_dims;
+
+/* Bytes of device workspace of each call for `dims` (256-byte aligned, not shared with a call that
+ * runs at the same time); 0 when the dims are invalid or unsupported. They hold the status word
+ * (ssd_mixer_workspace_status) and, where rows are cut into segments to fill the device, the state
+ * entering every segment; a backward pass with shared heads also T H (dk + dv) fp32 partial
+ * gradients. */
+SSD_API size_t ssd_mixer_linear_prefill_workspace_size(const ssd_linear_dims* dims);
+SSD_API size_t ssd_mixer_linear_prefill_varlen_workspace_size(const ssd_linear_dims* dims);
+SSD_API size_t ssd_mixer_linear_backward_workspace_size(const ssd_linear_dims* dims);
+
+/* Prefill: b independent rows of L tokens. init_state [b][H][dv][dk] or NULL = zeros; final_state
+ * the same shape, which may be init_state itself. L = 0: o is untouched, the final state is the
+ * initial one. */
+SSD_API ssd_status ssd_mixer_linear_prefill(const ssd_linear_dims* dims,
+                                            const void* q, int64_t q_ld,
+                                            const void* k, int64_t k_ld,
+                                            const void* v, int64_t v_ld,
+                                            const float* log_decay, const float* init_state,
+                                            void* o, int64_t o_ld, float* final_state,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Packed sequences on state slots, as ssd_mixer_prefill_varlen: dims->batch sequences, dims->seqlen
+ * = T packed rows, sequence i in rows cu_seqlens[i] .. cu_seqlens[i+1]-1 (int32, device, [b+1], not
+ * decreasing; lengths may be 0; rows behind the last sequence are left as they were), continuing
+ * from slot slot_idx[i] of state [nslots][H][dv][dk] where has_init[i] is nonzero (NULL: all) and
+ * starting from zeros elsewhere; the slot receives the final state. slot_idx NULL: slot i. A slot
+ * outside 0 .. nslots-1 skips its sequence (padding of a captured batch): neither its state nor its
+ * rows of o are written. The other slots must be distinct. Row offsets outside 0 .. T are clamped. */
+SSD_API ssd_status ssd_mixer_linear_prefill_varlen(const ssd_linear_dims* dims,
+                                                   const int32_t* cu_seqlens, const int32_t* slot_idx,
+                                                   const uint8_t* has_init,
+                                                   const void* q, int64_t q_ld,
+                                                   const void* k, int64_t k_ld,
+                                                   const void* v, int64_t v_ld,
+                                                   const float* log_decay, float* state, int64_t nslots,
+                                                   void* o, int64_t o_ld,
+                                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode: one token of each of b sequences (q [b][H][dk] ...), their states updated in place.
+ * Slots as for the packed prefill; dims->seqlen must be 1. Needs no workspace. */
+SSD_API ssd_status ssd_mixer_linear_decode_step(const ssd_linear_dims* dims,
+                                                const void* q, int64_t q_ld,
+                                                const void* k, int64_t k_ld,
+                                                const void* v, int64_t v_ld,
+                                                const float* log_decay, float* state, int64_t nslots,
+                                                const int32_t* slot_idx, void* o, int64_t o_ld, void* stream);
+
+/* Gradients of ssd_mixer_linear_prefill with respect to q, k, v and the initial state. dout
+ * [b][L][H][dv] is the gradient of o; dfinal_state [b][H][dv][dk] fp32 that of the final state, or
+ * NULL = zeros; init_state as in the forward call (NULL = zeros). dq, dk, dv are written, not added
+ * to, dk and dv summed over the heads that share them; dinit_state fp32 or NULL when not wanted.
+ * Nothing of the forward call is needed: the states are computed again. */
+SSD_API ssd_status ssd_mixer_linear_backward(const ssd_linear_dims* dims,
+                                             const void* q, int64_t q_ld,
+                                             const void* k, int64_t k_ld,
+                                             const void* v, int64_t v_ld,
+                                             const float* log_decay, const float* init_state,
+                                             const void* dout, int64_t dout_ld, const float* dfinal_state,
+                                             void* dq, int64_t dq_ld,
+                                             void* dk, int64_t dk_ld,
+                                             void* dv, int64_t dv_ld,
+                                             float* dinit_state,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm of rows x [rows][groups * width] (row stride x_ld elements, any element alignment) over
+ * each contiguous group of width channels: y = (x - mean) * rstd * weight + bias, rstd = 1 /
+ * sqrt(var + eps), eps >= 0. groups = 1 is the norm in front of a layer; groups = H normalises each
+ * head of an attention output. weight, bias [groups * width] fp32 or NULL (ones, zeros); mean, rstd
+ * [rows][groups] fp32 receive what the backward pass reads, or NULL. x, y of type act, sums in fp32;
+ * y may be x itself (same stride). (No counterpart in the pages, whose norms are RMS norms.) */
+SSD_API ssd_status ssd_mixer_layer_norm(int64_t rows, int32_t groups, int32_t width, float eps, int32_t act,
+                                        const void* x, int64_t x_ld, const float* weight, const float* bias,
+                                        void* y, int64_t y_ld, float* mean, float* rstd, void* stream);
+
+/* Bytes of device workspace of the layer norm's backward pass (256-byte aligned): the partial sums
+ * of the parameter gradients. 0 when the sizes are invalid or unsupported. */
+SSD_API size_t ssd_mixer_layer_norm_backward_workspace_size(int64_t rows, int32_t groups, int32_t width, int32_t act);
+
+/* Gradients of ssd_mixer_layer_norm from dy and the saved mean and rstd: dx of type act; dweight and
+ * dbias [groups * width] fp32, written, or NULL when not wanted (with both NULL no workspace is
+ * needed). The sums over the rows are taken in a fixed order: the same inputs give the same bits.
+ * rows = 0 gives zero parameter gradients. Outputs must not overlap inputs. */
+SSD_API ssd_status ssd_mixer_layer_norm_backward(int64_t rows, int32_t groups, int32_t width, int32_t act,
+                                                 const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
+                                                 const float* weight, const float* mean, const float* rstd,
+                                                 void* dx, int64_t dx_ld, float* dweight, float* dbias,
+                                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads the device status word that the prefill kernels keep at the start of
  * `workspace` (the last call that used it clears it on its stream before its first kernel,
  * and its kernels record the first failure). Synchronises `stream`. Returns SSD_OK;
