@@ -376,16 +376,33 @@ cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStr
     return cudaGetLastError();
 }
 
+// Splitting rows into segments fills SMs that whole rows would leave idle, at the price of a pass over
+// k and v (and a kernel that joins the states) before the main one. Times in units of one block of 128
+// tokens of the main pass: a CTA's start costs about one and a half, a block of the states' pass 0.6,
+// the joining kernel and two more launches about 3. The tensor-core scan runs one CTA per SM, the
+// CUDA-core one two or more.
 int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms)
 {
-    // Enough segments for every SM to have work, none under 128 tokens.
-    const int64_t want = (int64_t)sms * (tc ? 1 : 2);
-    const int64_t rows = b * H * nscans;
-    const int64_t len = packed ? T : L;
-    if (rows >= want || len <= 128) return len > 0 ? ((len + 127) / 128) * 128 + 128 : 128;
-    const int64_t per = packed ? (T * H * nscans + want - 1) / want : L / ((want + rows - 1) / rows);
-    const int64_t blocks = (per + 127) / 128;
-    return (blocks > 0 ? blocks : 1) * 128;
+    const int64_t rows = b * H * nscans, slots = tc ? sms : 2 * sms;
+    const int64_t blocks = ((packed ? T : L) + 127) / 128;
+    if (blocks <= 1 || b == 0) return 256;                 // nothing to split: longer than any row
+    // a packed row's length is not known here; they are taken as equal, and each may end in part of a segment
+    const int64_t per_row = packed ? (blocks + b - 1) / b : blocks;
+    double best = 0.0;
+    int64_t best_seg = 0;
+    for (int64_t nseg = 1; nseg <= per_row && nseg <= 256; ++nseg) {
+        const int64_t seg = (per_row + nseg - 1) / nseg;
+        if (best_seg && seg == best_seg) continue;
+        const int64_t n = packed ? (int64_t)H * nscans * (blocks / seg + (b + 1) / 2) : rows * ((per_row + seg - 1) / seg);
+        double cost = (double)((n + slots - 1) / slots) * (seg + 1.5);
+        if (seg < per_row) cost += (double)((n - rows > 0 ? n - rows + slots - 1 : slots) / slots) * (0.6 * seg + 1.5) + 3.0;
+        if (!best_seg || cost < best) {
+            best = cost;
+            best_seg = seg;
+        }
+    }
+    if (best_seg >= per_row && (!packed || b == 1)) return (blocks + 1) * 128;
+    return best_seg * 128;
 }
 
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,
@@ -412,8 +429,5 @@ cudaError_t launch_linear_decode(int64_t b, int H, int share, int DK, int DV, fl
     else launch_decode<float>(p, DK, b, st);
     return cudaGetLastError();
 }
-
-bool linear_tc_supported(const LinearScan&, int) { return false; }
-cudaError_t launch_linear_tc(const LinearCall&, const LinearScan*, int, cudaStream_t) { return cudaErrorNotSupported; }
 
 }  // namespace ssd

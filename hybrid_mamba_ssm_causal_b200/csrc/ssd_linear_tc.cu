@@ -1,0 +1,682 @@
+// ssd_linear_tc.cu -- the scan of linear attention on tcgen05 (bf16, DK and DV of 64 or 128).
+//
+// A CTA walks one segment of one (sequence, head) row in blocks of 128 tokens. With l the head's
+// decay, i and j tokens of the block counted in scan order, n its tokens and S [DV][DK] the state
+// that enters it:
+//   o_i = c sum_{j <= i} l^{i-j} u (q_i . k_j) v_j + c l^{i+1} S q_i
+//   S  <- l^n S + sum_j l^{n-1-j} u v_j k_j^T
+// (backwards the entering state has had its decay already: l^i S q_i, and l^n S + sum l^{n-j} u v_j k_j^T
+// leaves, decayed for the next block). Four products a block, all M = 128:
+//   QK     [i][j]  = Q K^T                       A, B: the TMA tiles, K-major
+//   inter  [i][d]  = Q S^T                       B: S in bf16, written by the state warps
+//   U      [d][e]  = (w V)^T K                   A: w V transposed, in TMEM; B: the K tile, MN-major
+//   intra  [i][d]  = P V                         A: the decayed scores P in TMEM; B: the V tile, MN-major
+// S stays in fp32 registers, S = l^n S + U, and w V is taken as the sum of three bf16 (24 bits), so
+// that the state is as exact as its fp32 sums; P and the operand copy of S are rounded to bf16 once,
+// which is as much as the rounding of o itself.
+//
+// Four warpgroups, so that the next block's w V and scores are under way while this one's state and
+// outputs are finished; registers are moved to the two that hold tiles (setmaxnreg):
+//   0  outputs, a row i each: scores -> P, then o = c l^{i+1} inter + intra, staged over the block's
+//      own tiles for a TMA store
+//   1  state, a row d each: S += U, and its operand copy
+//   2  w V: V's tile transposed by ldmatrix, times w, into TMEM, 32 tokens at a time in two slots
+//   3  one warp each for TMA loads, every MMA, and the stores
+// TMEM columns: QK and, over its first half, P; one output tile (inter is read out before intra
+// overwrites it); U; the two slots of w V.
+//
+// No decay factor is ever above 1: off the diagonal 32 x 32 tiles, l^{i-j} = l^{i-j0-31} l^{31-(j-j0)}.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "../../include/ssd_mixer.h"
+#include "ssd_common.cuh"
+#include "ssd_linear.h"
+#include "ssd_profile.h"
+#include "ssd_tc_util.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace tc;
+
+constexpr int kB = 128;                  // tokens per block
+constexpr int kThreads = 512;
+constexpr uint32_t kAtom = 128 * 128;    // one [128 rows][128 bytes] swizzled tile
+constexpr uint32_t kSmemMax = 232448;
+constexpr long long kWait = 4000000000LL;   // ~2 s at 2 GHz
+constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColV = 384;
+constexpr int kSub = 32;                 // tokens of one slot of w V
+constexpr uint32_t kSlotCols = 64;       // its TMEM columns: three terms of 16, and 16 unused
+// Registers per thread of the four warpgroups; they share what the launch gave them (512 x 128).
+constexpr int kRegsOut = 192, kRegsState = 184, kRegsV = 80, kRegsCtl = 48;
+static_assert(kRegsOut + kRegsState + kRegsV + kRegsCtl <= 4 * 128, "more registers than the launch's");
+
+template <int DK, int DV, bool STATES>
+struct Cfg {
+    static constexpr uint32_t kQ = STATES ? 0 : kAtom * (DK / 64), kK = kAtom * (DK / 64), kV = kAtom * (DV / 64);
+    static constexpr uint32_t kStage = kQ + kK + kV;
+    static constexpr uint32_t kS = STATES ? 0 : DV * DK * 2;
+    static constexpr uint32_t kTail = 2560;      // decay tables, barriers
+    static constexpr int kFit = (int)((kSmemMax - kS - kTail) / kStage);
+    static constexpr int kStages = kFit > 4 ? 4 : kFit;
+    static_assert(kStages >= 2, "two stages");
+    static constexpr uint32_t kOffS = kStages * kStage, kOffTab = kOffS + kS, kOffBar = kOffTab + 1712;
+    static constexpr uint32_t kSmem = kOffTab + kTail;
+};
+
+struct ScanMaps {
+    CUtensorMap q, k, v, o;
+};
+constexpr int kMaxScans = 3;
+struct TcArgs {
+    LinearCall c;
+    LinearScan s[kMaxScans];
+    int nscans;
+};
+struct TcMaps {
+    ScanMaps m[kMaxScans];
+};
+
+// MN-major operand in the 128-byte swizzled layout: rows of 64 elements along M or N (128 bytes), one
+// per K index. 8 rows make an atom of 1024 bytes; the next 64 elements along M or N start kAtom on.
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(kAtom >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Four 8 x 8 matrices of 16-bit elements, transposed: thread t holds, of each, column t / 4's
+// elements in rows 2 (t % 4) and 2 (t % 4) + 1. Thread 8 m + r gives the address of matrix m's row r.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 TMEM lanes x 16 columns: in each group of 4 columns, thread t writes column t % 4 of lanes t / 4
+// (first of the group's two registers) and t / 4 + 8 (second).
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t* v)
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+template <int DK, int DV, bool STATES>
+__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps)
+{
+    using C = Cfg<DK, DV, STATES>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const LinearCall& c = a.c;
+    const int z = blockIdx.x % a.nscans;
+    const int h = (int)((blockIdx.x / a.nscans) % c.H);
+    const int64_t item = blockIdx.x / a.nscans / c.H;
+    const LinearScan& s = a.s[z];
+    LinearItem it;
+    if (!linear_item(c, item, &it)) return;
+    const bool rev = s.reverse;
+    const bool last = rev ? it.seg == 0 : it.seg == it.nseg - 1;
+    if (STATES && last) return;
+
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // the same in a warp, as the compiler sees
+    const uint32_t sb = smem_u32(smem);
+    if (sb & 1023u) {
+        if (tid == 0) set_device_status(c.status, kDevSmemMisaligned);
+        return;
+    }
+    float* tab = reinterpret_cast<float*>(smem + C::kOffTab);      // l^0 .. l^128
+    float* ptab = tab + 132;                                       // the same times c u
+    float* wtab = ptab + 132;                                      // l^{31-x} (backwards l^x), x = 0 .. 31
+    float* vtab = wtab + 32;                                       // u l^{127-j} (backwards u l^{j+1}), j = 0 .. 127
+    const uint32_t bar0 = sb + C::kOffBar;
+    auto full = [&](int i) { return bar0 + 8 * i; };
+    auto empty = [&](int i) { return bar0 + 8 * (4 + i); };
+    auto v_ready = [&](int i) { return bar0 + 64 + 8 * i; };
+    auto v_free = [&](int i) { return bar0 + 80 + 8 * i; };
+    const uint32_t qk_done = bar0 + 96, p_ready = bar0 + 104, inter_done = bar0 + 112, inter_read = bar0 + 120,
+                   intra_done = bar0 + 128, o_free = bar0 + 136, o_staged = bar0 + 144, u_done = bar0 + 152,
+                   u_free = bar0 + 160, s_ready = bar0 + 168;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 176);
+    static_assert(C::kOffBar + 180 <= C::kSmem && C::kOffBar % 8 == 0 && C::kOffBar >= C::kOffTab + 424 * 4, "tail");
+
+    const int nb = (int)((it.n + kB - 1) / kB);
+    auto block = [&](int i) { return rev ? nb - 1 - i : i; };
+    auto tokens = [&](int b) { return it.n - (int64_t)b * kB < kB ? (int)(it.n - (int64_t)b * kB) : kB; };
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        mbar_init(qk_done, 1);
+        mbar_init(p_ready, 128);
+        mbar_init(inter_done, 1);
+        mbar_init(inter_read, 128);
+        mbar_init(intra_done, 1);
+        mbar_init(o_free, 128);
+        mbar_init(o_staged, 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(v_ready(i), 128);
+            mbar_init(v_free(i), 1);
+        }
+        mbar_init(u_done, 1);
+        mbar_init(u_free, 128);
+        mbar_init(s_ready, 128);
+        fence_mbar_init();
+    }
+    const double g = (double)linear_log_decay(c.log_decay, h);
+    if (tid <= kB) {
+        const double p = exp(g * tid);
+        tab[tid] = (float)p;
+        ptab[tid] = (float)(p * s.out_scale * s.u_scale);
+    } else if (tid >= 256 && tid < 288) {
+        wtab[tid - 256] = (float)exp(g * (rev ? tid - 256 : 287 - tid));
+    } else if (tid >= 384) {
+        vtab[tid - 384] = (float)(exp(g * (rev ? tid - 383 : 511 - tid)) * s.u_scale);
+    }
+    if (warp == 13) tmem_alloc(smem_u32(tmem_slot), 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    bool ok = true;
+    auto wait = [&](uint32_t bar, int n) {   // the barrier's n-th completion (from 0)
+        if (ok && !mbar_wait_bounded(bar, (uint32_t)(n & 1), kWait)) ok = false;
+    };
+
+    if (warp < 4) {
+        // ------------------------------------------------------------------ scores and outputs
+        regs_up<kRegsOut>();
+        if constexpr (!STATES) {
+            const int r = tid;                                     // row i of the block = TMEM lane
+            const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+            const float out_scale = s.out_scale;
+            const bool o_f32 = s.o_f32;
+            for (int i = 0; i < nb; ++i) {
+                const int st = i % C::kStages;
+                const int b = block(i), n = tokens(b);
+                wait(qk_done, i);
+                fence_after_sync();
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {                      // 32 score columns at a time
+                    uint32_t p[16];
+                    if (rev ? m < warp : m > warp) {               // all outside the mask
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) p[x] = 0;
+                    } else {
+                        float v[32];
+                        tmem_ld32(lanes + kColP + 32 * m, v);
+                        if (m == warp) {
+                            float w[32];
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) w[x] = ptab[rev ? max(x - lane, 0) : max(lane - x, 0)];
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) v[x] = (rev ? x >= lane : x <= lane) ? v[x] * w[x] : 0.0f;
+                        } else {
+                            const float2 f = splat2(ptab[rev ? 32 * m - r : r - 32 * m - 31]);
+                            float2 w[16];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float4 t = reinterpret_cast<const float4*>(wtab)[x];
+                                w[2 * x] = mul2(f, make_float2(t.x, t.y));
+                                w[2 * x + 1] = mul2(f, make_float2(t.z, t.w));
+                            }
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                const float2 t = mul2(make_float2(v[2 * x], v[2 * x + 1]), w[x]);
+                                v[2 * x] = t.x;
+                                v[2 * x + 1] = t.y;
+                            }
+                        }
+                        const int left = n - 32 * m;               // columns that are tokens
+                        if (left < 32) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) v[x] = x < left ? v[x] : 0.0f;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+                    }
+                    tmem_st16(lanes + kColP + 16 * m, p);
+                }
+                tmem_wait_st();
+                fence_before_sync();
+                mbar_arrive_local(p_ready);
+
+                float o[DV];
+                wait(inter_done, i);
+                fence_after_sync();
+#pragma unroll
+                for (int x = 0; x < DV; x += 32) tmem_ld32(lanes + kColO + x, o + x);
+                tmem_wait_ld();
+                fence_before_sync();
+                mbar_arrive_local(inter_read);
+                const int e = rev ? n - 1 - r : r + 1;
+                const float2 f = splat2(out_scale * tab[max(e, 0)]);   // rows past the sequence are not stored
+                wait(intra_done, i);
+                fence_after_sync();
+                unsigned char* so = smem + (size_t)st * C::kStage;   // over the block's tiles, which are done with
+#pragma unroll
+                for (int x = 0; x < DV; x += 16) {
+                    float v[16];
+                    tmem_ld16(lanes + kColO + x, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int y = 0; y < 16; y += 2) {
+                        const float2 t = fma2(f, make_float2(o[x + y], o[x + y + 1]), make_float2(v[y], v[y + 1]));
+                        v[y] = t.x;
+                        v[y + 1] = t.y;
+                    }
+                    if (o_f32) {                                     // tiles of 32 columns
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            *reinterpret_cast<float4*>(so + (x / 32) * kAtom + r * 128 + (((y + (x & 16) / 4) ^ (r & 7)) << 4)) =
+                                make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+                    } else {                                         // tiles of 64
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            *reinterpret_cast<uint4*>(so + (x / 64) * kAtom + r * 128 + (((y + (x & 48) / 8) ^ (r & 7)) << 4)) =
+                                make_uint4(pack_bf16x2(v[8 * y], v[8 * y + 1]), pack_bf16x2(v[8 * y + 2], v[8 * y + 3]),
+                                           pack_bf16x2(v[8 * y + 4], v[8 * y + 5]), pack_bf16x2(v[8 * y + 6], v[8 * y + 7]));
+                    }
+                }
+                fence_before_sync();
+                mbar_arrive_local(o_free);
+                if (n < kB) {   // rows behind the sequence may be another's: plain stores of its own rows
+                    named_sync(1, 128);
+                    const int64_t row = it.row0 + (int64_t)b * kB;
+                    const int es = s.o_f32 ? 4 : 2, chunks = DV * es / 16;
+                    unsigned char* dst = (unsigned char*)s.o;
+                    for (int id = tid; id < n * chunks; id += 128) {
+                        const int rr = id / chunks, ch = id % chunks;
+                        *reinterpret_cast<uint4*>(dst + ((row + rr) * s.o_ld + (int64_t)h * DV) * es + ch * 16) =
+                            *reinterpret_cast<const uint4*>(so + (ch >> 3) * kAtom + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                    }
+                }
+                fence_async_smem();
+                mbar_arrive_local(o_staged);
+            }
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------------ the state
+        regs_up<kRegsState>();
+        const int d = tid - 128;                                   // state row = TMEM lane
+        const uint32_t lanes = tmem + ((uint32_t)((warp - 4) * 32) << 16);
+        const bool mine = d < DV;
+        const int64_t hs = (int64_t)DK * DV;
+        float S[DK];
+#pragma unroll
+        for (int e = 0; e < DK; ++e) S[e] = 0.0f;
+        if (!STATES && mine) {
+            if (it.nseg > 1) {       // never the slot itself: the row's last segment may be rewriting it
+                const float4* p = reinterpret_cast<const float4*>(s.seg_states + (item * c.H + h) * hs + (int64_t)d * DK);
+#pragma unroll
+                for (int e = 0; e < DK / 4; ++e) {
+                    const float4 x = p[e];
+                    S[4 * e] = x.x; S[4 * e + 1] = x.y; S[4 * e + 2] = x.z; S[4 * e + 3] = x.w;
+                }
+            } else if (linear_has_init(c, s, it.seq)) {
+                const float* p = s.init + (it.slot * c.H + h) * hs + (int64_t)d * s.init_rs;
+                if (s.init_cs == 1) {
+#pragma unroll
+                    for (int e = 0; e < DK / 4; ++e) {
+                        const float4 x = reinterpret_cast<const float4*>(p)[e];
+                        S[4 * e] = x.x; S[4 * e + 1] = x.y; S[4 * e + 2] = x.z; S[4 * e + 3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < DK; e += 8) {       // 8 addresses at a time: more would not fit in registers
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) S[e + x] = p[x * s.init_cs];
+                        p += 8 * s.init_cs;
+                        asm volatile("" : "+l"(p)::"memory");
+                    }
+                }
+            }
+        }
+        auto publish = [&]() {       // S in bf16, the K-major operand of inter
+            if constexpr (!STATES) {
+                if (mine) {
+#pragma unroll
+                    for (int e = 0; e < DK; e += 8)
+                        *reinterpret_cast<uint4*>(smem + C::kOffS + (e / 64) * (DV * 128) + d * 128 + ((((e & 63) >> 3) ^ (d & 7)) << 4)) =
+                            make_uint4(pack_bf16x2(S[e], S[e + 1]), pack_bf16x2(S[e + 2], S[e + 3]),
+                                       pack_bf16x2(S[e + 4], S[e + 5]), pack_bf16x2(S[e + 6], S[e + 7]));
+                }
+                fence_async_smem();
+                mbar_arrive_local(s_ready);
+            }
+        };
+        if (nb > 0) publish();
+        const LinearDecay whole((float)(g * kB));
+        for (int i = 0; i < nb; ++i) {
+            const int n = tokens(block(i));
+            const LinearDecay dec = n == kB ? whole : LinearDecay((float)(g * n));
+            wait(u_done, i);
+            fence_after_sync();
+#pragma unroll
+            for (int e = 0; e < DK; e += 16) {
+                float u[16];
+                tmem_ld16(lanes + kColU + e, u);
+                tmem_wait_ld();
+                if (dec.slow) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) S[e + x] = fmaf(dec.f, S[e + x], S[e + x] + u[x]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) S[e + x] = fmaf(dec.f, S[e + x], u[x]);
+                }
+            }
+            fence_before_sync();
+            mbar_arrive_local(u_free);
+            if (i + 1 < nb) {
+                if (!STATES) wait(inter_done, i);        // the operand copy of S has been read
+                publish();
+            }
+        }
+        float* out = nullptr;
+        if (STATES) out = s.seg_states + (item * c.H + h) * hs;
+        else if (last && s.final_state) out = s.final_state + (it.slot * c.H + h) * hs;
+        if (out && mine) {
+            float4* p = reinterpret_cast<float4*>(out + (int64_t)d * DK);
+#pragma unroll
+            for (int e = 0; e < DK / 4; ++e) p[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------------ w V
+        regs_down<kRegsV>();
+        const int q = warp - 8;                                    // TMEM lanes, and rows d, 32 q ..
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + kColV;
+        const bool mine = 32 * q < DV;
+        if (!mine) {                                               // lanes past DV: zeros, once
+            uint32_t zero[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) zero[x] = 0;
+#pragma unroll
+            for (uint32_t x = 0; x < 2 * kSlotCols; x += 16) tmem_st16(lanes + x, zero);
+            tmem_wait_st();
+        }
+        for (int i = 0; i < nb; ++i) {
+            const int st = i % C::kStages;
+            const int n = tokens(block(i));
+            const uint32_t ok_off = (uint32_t)st * C::kStage + C::kQ, ov_off = ok_off + C::kK;
+            wait(full(st), i / C::kStages);
+            if (n < kB) {            // rows behind the sequence: whatever they hold must not meet a zero weight
+                for (int id = tid - 256; id < (kB - n) * 8; id += 128) {
+                    const int rr = n + (id >> 3), ch = (id & 7) << 4;
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(smem + ok_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int x = 0; x < DV / 64; ++x) *reinterpret_cast<uint4*>(smem + ov_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
+                }
+                named_sync(2, 128);
+                fence_async_smem();
+            }
+#pragma unroll 1
+            for (int u = 0; u < kB / kSub; ++u) {
+                const int k = i * (kB / kSub) + u;
+                if (k >= 2) wait(v_free(k & 1), (k >> 1) - 1);
+                fence_after_sync();
+                if (mine) {
+                    // thread t's tokens of 8-token group x: j0 + 8 x, and the next. A short block is the
+                    // end of a row: forwards its weights are the last n. Rows behind it are zeros by
+                    // now, whatever weight they meet.
+                    const int j0 = u * kSub + 2 * (lane & 3) + (rev ? 0 : kB - n);
+                    float2 w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[x] = make_float2(vtab[min(j0 + 8 * x, kB - 1)], vtab[min(j0 + 8 * x + 1, kB - 1)]);
+                    // addresses: matrix m = lane / 8 is token group m, its row lane % 8 a token
+                    const uint32_t row = (uint32_t)(u * kSub + lane);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {          // 16 rows d
+                        uint32_t raw[2][4], a0[8], a1[8], a2[8];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t ch = (uint32_t)(q * 4 + half * 2 + y);     // 8-column group of d
+                            ldmatrix_x4_trans(sb + ov_off + (ch >> 3) * kAtom + row * 128 + (((ch & 7) ^ (row & 7)) << 4), raw[y]);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float2 v = bf2_to_f2(raw[y][x]);
+                                float2 t = mul2(v, w[x]);
+                                const uint32_t h0 = pack_f2(t);
+                                float2 b0 = bf2_to_f2(h0);
+                                t = make_float2(t.x - b0.x, t.y - b0.y);
+                                const uint32_t h1 = pack_f2(t);
+                                b0 = bf2_to_f2(h1);
+                                a0[2 * x + y] = h0;
+                                a1[2 * x + y] = h1;
+                                a2[2 * x + y] = pack_bf16x2(t.x - b0.x, t.y - b0.y);
+                            }
+                        const uint32_t at = lanes + ((uint32_t)(half * 16) << 16) + (uint32_t)(k & 1) * kSlotCols;
+                        tmem_st_16x128b_x4(at, a0);
+                        tmem_st_16x128b_x4(at + 16, a1);
+                        tmem_st_16x128b_x4(at + 32, a2);
+                    }
+                    tmem_wait_st();
+                }
+                fence_before_sync();
+                mbar_arrive_local(v_ready(k & 1));
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------ one thread each
+        regs_down<kRegsCtl>();
+        if (warp == 12 && lane == 0) {                             // loads
+            const ScanMaps& m = maps.m[z];
+            for (int i = 0; i < nb; ++i) {
+                const int st = i % C::kStages;
+                if (i >= C::kStages) wait(empty(st), i / C::kStages - 1);
+                mbar_arrive_expect_tx(full(st), C::kStage);
+                const uint32_t dst = sb + (uint32_t)st * C::kStage;
+                const int row = (int)(it.row0 + (int64_t)block(i) * kB);
+                if constexpr (!STATES)
+                    for (int x = 0; x < DK / 64; ++x)
+                        tma_load_3d(dst + x * kAtom, &m.q, (h / s.q_share) * DK + 64 * x, row, 0, full(st));
+                for (int x = 0; x < DK / 64; ++x)
+                    tma_load_3d(dst + C::kQ + x * kAtom, &m.k, (h / s.k_share) * DK + 64 * x, row, 0, full(st));
+                for (int x = 0; x < DV / 64; ++x)
+                    tma_load_3d(dst + C::kQ + C::kK + x * kAtom, &m.v, (h / s.v_share) * DV + 64 * x, row, 0, full(st));
+            }
+        } else if (warp == 13) {                                   // MMAs: the warp waits, one lane issues
+            const bool leader = elect_one();
+            for (int i = 0; i < nb; ++i) {
+                const int st = i % C::kStages;
+                const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK, ss = sb + C::kOffS;
+                // descriptors count addresses in 16 bytes
+                const uint64_t kmn = sdesc_sw128_mn(sk);
+                wait(full(st), i / C::kStages);
+                fence_after_sync();
+                if constexpr (!STATES) {
+                    const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), sd = sdesc_sw128(ss);
+                    if (leader) {
+#pragma unroll
+                        for (int x = 0; x < DK / 16; ++x) {
+                            const uint64_t at = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
+                            mma_bf16(tmem + kColP, qd + at, kd + at, idesc_bf16(128, 128, 0, 0), x > 0);
+                        }
+                        mma_commit(qk_done);
+                    }
+                    __syncwarp();
+                    wait(s_ready, i);
+                    if (i > 0) wait(o_free, i - 1);
+                    fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int x = 0; x < DK / 16; ++x)
+                            mma_bf16(tmem + kColO, qd + (((x >> 2) * kAtom + (x & 3) * 32) >> 4),
+                                     sd + (((x >> 2) * (DV * 128) + (x & 3) * 32) >> 4), idesc_bf16(128, DV, 0, 0), x > 0);
+                        mma_commit(inter_done);
+                    }
+                    __syncwarp();
+                }
+                if (i > 0) wait(u_free, i - 1);
+#pragma unroll 1
+                for (int u = 0; u < kB / kSub; ++u) {
+                    const int k = i * (kB / kSub) + u;
+                    wait(v_ready(k & 1), k >> 1);
+                    fence_after_sync();
+                    const uint32_t at = tmem + kColV + (uint32_t)(k & 1) * kSlotCols;
+                    if (leader) {
+#pragma unroll
+                        for (int x = 0; x < kSub / 16; ++x)
+#pragma unroll
+                            for (int t = 0; t < 3; ++t)
+                                mma_bf16_ts(tmem + kColU, at + t * 16 + x * 8, kmn + (uint64_t)((u * kSub + x * 16) * 128 >> 4),
+                                            idesc_bf16(128, DK, 0, 1), u + x + t > 0);
+                        mma_commit(v_free(k & 1));
+                        if (u == kB / kSub - 1) {
+                            mma_commit(u_done);
+                            if (STATES) mma_commit(empty(st));
+                        }
+                    }
+                    __syncwarp();
+                }
+                if constexpr (!STATES) {
+                    wait(p_ready, i);
+                    wait(inter_read, i);
+                    fence_after_sync();
+                    const uint64_t vmn = sdesc_sw128_mn(sv);
+                    if (leader) {
+#pragma unroll
+                        for (int x = 0; x < kB / 16; ++x)
+                            mma_bf16_ts(tmem + kColO, tmem + kColP + x * 8, vmn + (uint64_t)(x * 2048 >> 4), idesc_bf16(128, DV, 0, 1), x > 0);
+                        mma_commit(intra_done);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (warp == 14 && lane == 0 && !STATES) {           // stores
+            const int per = s.o_f32 ? 32 : 64;
+            for (int i = 0; i < nb; ++i) {
+                const int st = i % C::kStages, b = block(i);
+                wait(o_staged, i);
+                if (tokens(b) == kB) {
+                    for (int x = 0; x < DV / per; ++x)
+                        tma_store_3d(&maps.m[z].o, sb + (uint32_t)st * C::kStage + x * kAtom, h * DV + per * x,
+                                     (int)(it.row0 + (int64_t)b * kB), 0);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+                mbar_arrive_local(empty(st));
+            }
+            bulk_wait_all();
+        }
+    }
+    if (!ok) set_device_status(c.status, kDevTimeout);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = []() -> EncodeFn {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// rows x cols of bf16 (or fp32), in boxes of 128 rows x 128 bytes, 128-byte swizzled.
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, bool f32)
+{
+    EncodeFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t es = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * es, (cuuint64_t)(rows * ld) * es};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / es), kB, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV, bool STATES>
+cudaError_t launch_one(const TcArgs& a, const TcMaps& m, cudaStream_t st)
+{
+    using C = Cfg<DK, DV, STATES>;
+    cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<DK, DV, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    LaunchScope ls(STATES ? "linear_tc_states" : "linear_tc", st);
+    linear_tc_kernel<DK, DV, STATES><<<(unsigned)(a.c.items * a.c.H * a.nscans), kThreads, C::kSmem, st>>>(a, m);
+    return cudaGetLastError();
+}
+
+template <int DK, int DV>
+cudaError_t launch_shape(const TcArgs& a, const TcMaps& m, cudaStream_t st)
+{
+    if (a.c.split) {
+        cudaError_t e = launch_one<DK, DV, true>(a, m, st);
+        for (int i = 0; i < a.nscans && e == cudaSuccess; ++i) e = launch_linear_pass(a.c, a.s[i], st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_one<DK, DV, false>(a, m, st);
+}
+
+}  // namespace
+
+bool linear_tc_supported(const LinearScan& s, int act)
+{
+    return act == SSD_BF16 && (s.DK == 64 || s.DK == 128) && (s.DV == 64 || s.DV == 128);
+}
+
+cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st)
+{
+    if (c.items == 0) return cudaSuccess;
+    bool done[kMaxScans] = {};
+    for (int i = 0; i < nscans; ++i) {   // scans of one shape run in the same launches
+        if (done[i]) continue;
+        TcArgs a{};
+        TcMaps m;
+        memset(&m, 0, sizeof(m));
+        a.c = c;
+        for (int j = i; j < nscans; ++j) {
+            const LinearScan& s = scans[j];
+            if (done[j] || s.DK != scans[i].DK || s.DV != scans[i].DV) continue;
+            done[j] = true;
+            a.s[a.nscans] = s;
+            ScanMaps& x = m.m[a.nscans++];
+            if (c.T > 0 && (!encode_rows(&x.q, s.q, c.T, (int64_t)(c.H / s.q_share) * s.DK, s.q_ld, false) ||
+                            !encode_rows(&x.k, s.k, c.T, (int64_t)(c.H / s.k_share) * s.DK, s.k_ld, false) ||
+                            !encode_rows(&x.v, s.v, c.T, (int64_t)(c.H / s.v_share) * s.DV, s.v_ld, false) ||
+                            !encode_rows(&x.o, s.o, c.T, (int64_t)c.H * s.DV, s.o_ld, s.o_f32)))
+                return cudaErrorInvalidValue;
+        }
+        const int dk = scans[i].DK, dv = scans[i].DV;
+        const cudaError_t e = dk == 64 ? (dv == 64 ? launch_shape<64, 64>(a, m, st) : launch_shape<64, 128>(a, m, st))
+                                       : (dv == 64 ? launch_shape<128, 64>(a, m, st) : launch_shape<128, 128>(a, m, st));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace ssd
