@@ -51,7 +51,7 @@ constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColV = 384;
 constexpr int kSub = 32;                 // tokens of one slot of w V
 constexpr uint32_t kSlotCols = 64;       // its TMEM columns: three terms of 16, and 16 unused
 // Registers per thread of the four warpgroups; they share what the launch gave them (512 x 128).
-constexpr int kRegsOut = 192, kRegsState = 184, kRegsV = 80, kRegsCtl = 48;
+constexpr int kRegsOut = 208, kRegsState = 184, kRegsV = 72, kRegsCtl = 48;
 static_assert(kRegsOut + kRegsState + kRegsV + kRegsCtl <= 4 * 128, "more registers than the launch's");
 
 template <int DK, int DV, bool STATES>
@@ -144,15 +144,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     float* wtab = ptab + 132;                                      // l^{31-x} (backwards l^x), x = 0 .. 31
     float* vtab = wtab + 32;                                       // u l^{127-j} (backwards u l^{j+1}), j = 0 .. 127
     const uint32_t bar0 = sb + C::kOffBar;
-    auto full = [&](int i) { return bar0 + 8 * i; };
-    auto empty = [&](int i) { return bar0 + 8 * (4 + i); };
-    auto v_ready = [&](int i) { return bar0 + 64 + 8 * i; };
-    auto v_free = [&](int i) { return bar0 + 80 + 8 * i; };
-    const uint32_t qk_done = bar0 + 96, p_ready = bar0 + 104, inter_done = bar0 + 112, inter_read = bar0 + 120,
-                   intra_done = bar0 + 128, o_free = bar0 + 136, o_staged = bar0 + 144, u_done = bar0 + 152,
-                   u_free = bar0 + 160, s_ready = bar0 + 168;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 176);
-    static_assert(C::kOffBar + 180 <= C::kSmem && C::kOffBar % 8 == 0 && C::kOffBar >= C::kOffTab + 424 * 4, "tail");
+    auto q_full = [&](int i) { return bar0 + 8 * i; };
+    auto q_empty = [&](int i) { return bar0 + 32 + 8 * i; };
+    auto kv_full = [&](int i) { return bar0 + 64 + 8 * i; };
+    auto kv_empty = [&](int i) { return bar0 + 96 + 8 * i; };
+    auto v_ready = [&](int i) { return bar0 + 128 + 8 * i; };
+    auto v_free = [&](int i) { return bar0 + 144 + 8 * i; };
+    const uint32_t qk_done = bar0 + 160, p_ready = bar0 + 168, inter_done = bar0 + 176, inter_read = bar0 + 184,
+                   intra_done = bar0 + 192, o_free = bar0 + 200, o_staged = bar0 + 208, u_done = bar0 + 216,
+                   u_free = bar0 + 224, s_ready = bar0 + 232;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 240);
+    static_assert(C::kOffBar + 244 <= C::kSmem && C::kOffBar % 8 == 0 && C::kOffBar >= C::kOffTab + 424 * 4, "tail");
 
     const int nb = (int)((it.n + kB - 1) / kB);
     auto block = [&](int i) { return rev ? nb - 1 - i : i; };
@@ -160,8 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(full(i), 1);
-            mbar_init(empty(i), 1);
+            mbar_init(q_full(i), 1);
+            mbar_init(q_empty(i), 1);
+            mbar_init(kv_full(i), 1);
+            mbar_init(kv_empty(i), 1);
         }
         mbar_init(qk_done, 1);
         mbar_init(p_ready, 128);
@@ -194,12 +198,97 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // o is staged over Q's tiles; k's and v's are free as soon as the block's MMAs are done, unless o
+    // is larger than q
+    const bool kv_early = STATES || (DV <= DK && !s.o_f32);
     bool ok = true;
     auto wait = [&](uint32_t bar, int n) {   // the barrier's n-th completion (from 0)
         if (ok && !mbar_wait_bounded(bar, (uint32_t)(n & 1), kWait)) ok = false;
     };
 
-    if (warp < 4) {
+    if (STATES ? warp < 4 || (warp >= 8 && warp < 12) : warp >= 8 && warp < 12) {
+        // ------------------------------------------------------------------ w V
+        // where no outputs are wanted, warpgroup 0 takes every other sub-block (and slot)
+        regs_down<kRegsV>();
+        const int first = STATES && warp < 4 ? 1 : 0, step = STATES ? 2 : 1;
+        const int q = warp & 3;                                    // TMEM lanes, and rows d, 32 q ..
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + kColV;
+        const bool mine = 32 * q < DV;
+        if (!mine) {                                               // lanes past DV: zeros, once
+            uint32_t zero[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) zero[x] = 0;
+#pragma unroll
+            for (uint32_t x = 0; x < 2 * kSlotCols; x += 16) tmem_st16(lanes + x, zero);
+            tmem_wait_st();
+        }
+        for (int i = 0; i < nb; ++i) {
+            const int st = i % C::kStages;
+            const int n = tokens(block(i));
+            const uint32_t ok_off = (uint32_t)st * C::kStage + C::kQ, ov_off = ok_off + C::kK;
+            wait(kv_full(st), i / C::kStages);
+            if (n < kB && first == 0) {   // rows behind the sequence: whatever they hold must not meet a zero weight
+                for (int id = tid & 127; id < (kB - n) * 8; id += 128) {
+                    const int rr = n + (id >> 3), ch = (id & 7) << 4;
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(smem + ok_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int x = 0; x < DV / 64; ++x) *reinterpret_cast<uint4*>(smem + ov_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
+                }
+                named_sync(2, 128);
+                fence_async_smem();
+            }
+            if (n < kB && step == 2) named_sync(3, 256);
+#pragma unroll 1
+            for (int u = first; u < kB / kSub; u += step) {
+                const int k = i * (kB / kSub) + u;
+                if (k >= 2) wait(v_free(k & 1), (k >> 1) - 1);
+                fence_after_sync();
+                if (mine) {
+                    // thread t's tokens of 8-token group x: j0 + 8 x, and the next. A short block is the
+                    // end of a row: forwards its weights are the last n. Rows behind it are zeros by
+                    // now, whatever weight they meet.
+                    const int j0 = u * kSub + 2 * (lane & 3) + (rev ? 0 : kB - n);
+                    float2 w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[x] = make_float2(vtab[min(j0 + 8 * x, kB - 1)], vtab[min(j0 + 8 * x + 1, kB - 1)]);
+                    // addresses: matrix m = lane / 8 is token group m, its row lane % 8 a token
+                    const uint32_t row = (uint32_t)(u * kSub + lane);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {          // 16 rows d
+                        uint32_t raw[2][4], a0[8], a1[8], a2[8];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t ch = (uint32_t)(q * 4 + half * 2 + y);     // 8-column group of d
+                            ldmatrix_x4_trans(sb + ov_off + (ch >> 3) * kAtom + row * 128 + (((ch & 7) ^ (row & 7)) << 4), raw[y]);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float2 v = bf2_to_f2(raw[y][x]);
+                                float2 t = mul2(v, w[x]);
+                                const uint32_t h0 = pack_f2(t);
+                                float2 b0 = bf2_to_f2(h0);
+                                t = make_float2(t.x - b0.x, t.y - b0.y);
+                                const uint32_t h1 = pack_f2(t);
+                                b0 = bf2_to_f2(h1);
+                                a0[2 * x + y] = h0;
+                                a1[2 * x + y] = h1;
+                                a2[2 * x + y] = pack_bf16x2(t.x - b0.x, t.y - b0.y);
+                            }
+                        const uint32_t at = lanes + ((uint32_t)(half * 16) << 16) + (uint32_t)(k & 1) * kSlotCols;
+                        tmem_st_16x128b_x4(at, a0);
+                        tmem_st_16x128b_x4(at + 16, a1);
+                        tmem_st_16x128b_x4(at + 32, a2);
+                    }
+                    tmem_wait_st();
+                }
+                fence_before_sync();
+                mbar_arrive_local(v_ready(k & 1));
+            }
+        }
+    } else if (!STATES && warp < 4) {
         // ------------------------------------------------------------------ scores and outputs
         regs_up<kRegsOut>();
         if constexpr (!STATES) {
@@ -212,46 +301,44 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const int b = block(i), n = tokens(b);
                 wait(qk_done, i);
                 fence_after_sync();
+                // 32 score columns at a time. The loops here are kept rolled where registers allow: four
+                // warpgroups' code competes for the instruction cache.
 #pragma unroll 1
-                for (int m = 0; m < 4; ++m) {                      // 32 score columns at a time
+                for (int m = 0; m < 4; ++m) {
                     uint32_t p[16];
                     if (rev ? m < warp : m > warp) {               // all outside the mask
 #pragma unroll
                         for (int x = 0; x < 16; ++x) p[x] = 0;
                     } else {
-                        float v[32];
-                        tmem_ld32(lanes + kColP + 32 * m, v);
+                        float a[32];
+                        tmem_ld32(lanes + kColP + 32 * m, a);
+                        tmem_wait_ld();
                         if (m == warp) {
-                            float w[32];
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) w[x] = ptab[rev ? max(x - lane, 0) : max(lane - x, 0)];
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) v[x] = (rev ? x >= lane : x <= lane) ? v[x] * w[x] : 0.0f;
+                            for (int x = 0; x < 32; ++x) {
+                                const float t = a[x] * ptab[rev ? max(x - lane, 0) : max(lane - x, 0)];
+                                a[x] = (rev ? x >= lane : x <= lane) ? t : 0.0f;
+                            }
                         } else {
                             const float2 f = splat2(ptab[rev ? 32 * m - r : r - 32 * m - 31]);
-                            float2 w[16];
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
                                 const float4 t = reinterpret_cast<const float4*>(wtab)[x];
-                                w[2 * x] = mul2(f, make_float2(t.x, t.y));
-                                w[2 * x + 1] = mul2(f, make_float2(t.z, t.w));
-                            }
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const float2 t = mul2(make_float2(v[2 * x], v[2 * x + 1]), w[x]);
-                                v[2 * x] = t.x;
-                                v[2 * x + 1] = t.y;
+                                const float2 t0 = mul2(mul2(f, make_float2(t.x, t.y)), make_float2(a[4 * x], a[4 * x + 1]));
+                                const float2 t1 = mul2(mul2(f, make_float2(t.z, t.w)), make_float2(a[4 * x + 2], a[4 * x + 3]));
+                                a[4 * x] = t0.x;
+                                a[4 * x + 1] = t0.y;
+                                a[4 * x + 2] = t1.x;
+                                a[4 * x + 3] = t1.y;
                             }
                         }
                         const int left = n - 32 * m;               // columns that are tokens
                         if (left < 32) {
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) v[x] = x < left ? v[x] : 0.0f;
+                            for (int x = 0; x < 32; ++x) a[x] = x < left ? a[x] : 0.0f;
                         }
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+                        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(a[2 * x], a[2 * x + 1]);
                     }
                     tmem_st16(lanes + kColP + 16 * m, p);
                 }
@@ -272,11 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 wait(intra_done, i);
                 fence_after_sync();
                 unsigned char* so = smem + (size_t)st * C::kStage;   // over the block's tiles, which are done with
+                float y2[2][16];
+                tmem_ld16(lanes + kColO, y2[0]);
 #pragma unroll
                 for (int x = 0; x < DV; x += 16) {
-                    float v[16];
-                    tmem_ld16(lanes + kColO + x, v);
+                    float* v = y2[(x >> 4) & 1];
                     tmem_wait_ld();
+                    if (x + 16 < DV) tmem_ld16(lanes + kColO + x + 16, y2[((x >> 4) + 1) & 1]);
 #pragma unroll
                     for (int y = 0; y < 16; y += 2) {
                         const float2 t = fma2(f, make_float2(o[x + y], o[x + y + 1]), make_float2(v[y], v[y + 1]));
@@ -368,19 +457,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         for (int i = 0; i < nb; ++i) {
             const int n = tokens(block(i));
             const LinearDecay dec = n == kB ? whole : LinearDecay((float)(g * n));
+            const float2 f2 = splat2(dec.f), keep2 = splat2(dec.slow ? 1.0f : 0.0f);
             wait(u_done, i);
             fence_after_sync();
+            float u2[2][16];
+            tmem_ld16(lanes + kColU, u2[0]);
 #pragma unroll
             for (int e = 0; e < DK; e += 16) {
-                float u[16];
-                tmem_ld16(lanes + kColU + e, u);
+                float* u = u2[(e >> 4) & 1];
                 tmem_wait_ld();
-                if (dec.slow) {
+                if (e + 16 < DK) tmem_ld16(lanes + kColU + e + 16, u2[((e >> 4) + 1) & 1]);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) S[e + x] = fmaf(dec.f, S[e + x], S[e + x] + u[x]);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) S[e + x] = fmaf(dec.f, S[e + x], u[x]);
+                for (int x = 0; x < 16; x += 2) {          // LinearDecay::step, both kinds in one code
+                    const float2 S2 = make_float2(S[e + x], S[e + x + 1]);
+                    const float2 t = fma2(f2, S2, fma2(keep2, S2, make_float2(u[x], u[x + 1])));
+                    S[e + x] = t.x;
+                    S[e + x + 1] = t.y;
                 }
             }
             fence_before_sync();
@@ -398,85 +490,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 #pragma unroll
             for (int e = 0; e < DK / 4; ++e) p[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------------------------ w V
-        regs_down<kRegsV>();
-        const int q = warp - 8;                                    // TMEM lanes, and rows d, 32 q ..
-        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + kColV;
-        const bool mine = 32 * q < DV;
-        if (!mine) {                                               // lanes past DV: zeros, once
-            uint32_t zero[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) zero[x] = 0;
-#pragma unroll
-            for (uint32_t x = 0; x < 2 * kSlotCols; x += 16) tmem_st16(lanes + x, zero);
-            tmem_wait_st();
-        }
-        for (int i = 0; i < nb; ++i) {
-            const int st = i % C::kStages;
-            const int n = tokens(block(i));
-            const uint32_t ok_off = (uint32_t)st * C::kStage + C::kQ, ov_off = ok_off + C::kK;
-            wait(full(st), i / C::kStages);
-            if (n < kB) {            // rows behind the sequence: whatever they hold must not meet a zero weight
-                for (int id = tid - 256; id < (kB - n) * 8; id += 128) {
-                    const int rr = n + (id >> 3), ch = (id & 7) << 4;
-#pragma unroll
-                    for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(smem + ok_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int x = 0; x < DV / 64; ++x) *reinterpret_cast<uint4*>(smem + ov_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
-                }
-                named_sync(2, 128);
-                fence_async_smem();
-            }
-#pragma unroll 1
-            for (int u = 0; u < kB / kSub; ++u) {
-                const int k = i * (kB / kSub) + u;
-                if (k >= 2) wait(v_free(k & 1), (k >> 1) - 1);
-                fence_after_sync();
-                if (mine) {
-                    // thread t's tokens of 8-token group x: j0 + 8 x, and the next. A short block is the
-                    // end of a row: forwards its weights are the last n. Rows behind it are zeros by
-                    // now, whatever weight they meet.
-                    const int j0 = u * kSub + 2 * (lane & 3) + (rev ? 0 : kB - n);
-                    float2 w[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] = make_float2(vtab[min(j0 + 8 * x, kB - 1)], vtab[min(j0 + 8 * x + 1, kB - 1)]);
-                    // addresses: matrix m = lane / 8 is token group m, its row lane % 8 a token
-                    const uint32_t row = (uint32_t)(u * kSub + lane);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {          // 16 rows d
-                        uint32_t raw[2][4], a0[8], a1[8], a2[8];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t ch = (uint32_t)(q * 4 + half * 2 + y);     // 8-column group of d
-                            ldmatrix_x4_trans(sb + ov_off + (ch >> 3) * kAtom + row * 128 + (((ch & 7) ^ (row & 7)) << 4), raw[y]);
-                        }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const float2 v = bf2_to_f2(raw[y][x]);
-                                float2 t = mul2(v, w[x]);
-                                const uint32_t h0 = pack_f2(t);
-                                float2 b0 = bf2_to_f2(h0);
-                                t = make_float2(t.x - b0.x, t.y - b0.y);
-                                const uint32_t h1 = pack_f2(t);
-                                b0 = bf2_to_f2(h1);
-                                a0[2 * x + y] = h0;
-                                a1[2 * x + y] = h1;
-                                a2[2 * x + y] = pack_bf16x2(t.x - b0.x, t.y - b0.y);
-                            }
-                        const uint32_t at = lanes + ((uint32_t)(half * 16) << 16) + (uint32_t)(k & 1) * kSlotCols;
-                        tmem_st_16x128b_x4(at, a0);
-                        tmem_st_16x128b_x4(at + 16, a1);
-                        tmem_st_16x128b_x4(at + 32, a2);
-                    }
-                    tmem_wait_st();
-                }
-                fence_before_sync();
-                mbar_arrive_local(v_ready(k & 1));
-            }
-        }
     } else {
         // ------------------------------------------------------------------ one thread each
         regs_down<kRegsCtl>();
@@ -484,17 +497,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             const ScanMaps& m = maps.m[z];
             for (int i = 0; i < nb; ++i) {
                 const int st = i % C::kStages;
-                if (i >= C::kStages) wait(empty(st), i / C::kStages - 1);
-                mbar_arrive_expect_tx(full(st), C::kStage);
                 const uint32_t dst = sb + (uint32_t)st * C::kStage;
                 const int row = (int)(it.row0 + (int64_t)block(i) * kB);
-                if constexpr (!STATES)
-                    for (int x = 0; x < DK / 64; ++x)
-                        tma_load_3d(dst + x * kAtom, &m.q, (h / s.q_share) * DK + 64 * x, row, 0, full(st));
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_3d(dst + C::kQ + x * kAtom, &m.k, (h / s.k_share) * DK + 64 * x, row, 0, full(st));
+                if (i >= C::kStages) wait(kv_empty(st), i / C::kStages - 1);
+                mbar_arrive_expect_tx(kv_full(st), C::kK + C::kV);
                 for (int x = 0; x < DV / 64; ++x)
-                    tma_load_3d(dst + C::kQ + C::kK + x * kAtom, &m.v, (h / s.v_share) * DV + 64 * x, row, 0, full(st));
+                    tma_load_3d(dst + C::kQ + C::kK + x * kAtom, &m.v, (h / s.v_share) * DV + 64 * x, row, 0, kv_full(st));
+                for (int x = 0; x < DK / 64; ++x)
+                    tma_load_3d(dst + C::kQ + x * kAtom, &m.k, (h / s.k_share) * DK + 64 * x, row, 0, kv_full(st));
+                if constexpr (!STATES) {
+                    if (i >= C::kStages) wait(q_empty(st), i / C::kStages - 1);
+                    mbar_arrive_expect_tx(q_full(st), C::kQ);
+                    for (int x = 0; x < DK / 64; ++x)
+                        tma_load_3d(dst + x * kAtom, &m.q, (h / s.q_share) * DK + 64 * x, row, 0, q_full(st));
+                }
             }
         } else if (warp == 13) {                                   // MMAs: the warp waits, one lane issues
             const bool leader = elect_one();
@@ -503,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK, ss = sb + C::kOffS;
                 // descriptors count addresses in 16 bytes
                 const uint64_t kmn = sdesc_sw128_mn(sk);
-                wait(full(st), i / C::kStages);
+                wait(kv_full(st), i / C::kStages);
+                if (!STATES) wait(q_full(st), i / C::kStages);
                 fence_after_sync();
                 if constexpr (!STATES) {
                     const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), sd = sdesc_sw128(ss);
@@ -545,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         mma_commit(v_free(k & 1));
                         if (u == kB / kSub - 1) {
                             mma_commit(u_done);
-                            if (STATES) mma_commit(empty(st));
+                            if (STATES) mma_commit(kv_empty(st));
                         }
                     }
                     __syncwarp();
@@ -560,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         for (int x = 0; x < kB / 16; ++x)
                             mma_bf16_ts(tmem + kColO, tmem + kColP + x * 8, vmn + (uint64_t)(x * 2048 >> 4), idesc_bf16(128, DV, 0, 1), x > 0);
                         mma_commit(intra_done);
+                        if (kv_early) mma_commit(kv_empty(st));
                     }
                     __syncwarp();
                 }
@@ -576,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     bulk_commit();
                     bulk_wait_read_all();
                 }
-                mbar_arrive_local(empty(st));
+                mbar_arrive_local(q_empty(st));
+                if (!kv_early) mbar_arrive_local(kv_empty(st));
             }
             bulk_wait_all();
         }
