@@ -5,15 +5,16 @@
 //   dx = r (dh - mean(dh) - xh mean(dh xh)),   dw = sum over rows of dy xh,   db = sum of dy
 // All sums in fp32, the variance around the mean (no difference of large sums).
 //
-// Both passes are bound by memory: x (and dy) are read once into registers and y (dx) written once.
-// A thread holds NV vectors of 16 (or, for rows that only 8 divides, 8) bytes of its row; a group is
-// summed by a team, either a power of two of lanes of one warp (head norms: no barrier at all) or
-// the whole block. Rows that are not so aligned, and teams that would not fit, take a loop of one
-// warp per (row, group).
-// Forwards a block runs one row, or (lane teams) four rows whose loads are all in flight before the
-// first sum; the other blocks of the SM hide its latency. Backwards a block keeps its columns'
-// weight gradients in registers over many rows, the coming rows on their way into shared memory,
-// and leaves one partial sum; a second kernel adds those in a fixed order.
+// Both passes are bound by memory in principle, x (and dy) read once and y (dx) written once, and by
+// instructions in practice: few operations an element and few shuffles a row decide. A thread holds NV
+// vectors of 16 (or, for rows that only 8 divides, 8) bytes of a row; a group is summed by a team,
+// either a power of two of lanes of one warp (head norms: no barrier at all) or the whole block.
+// Rows that are not so aligned, and teams that would not fit, take a loop of one warp per (row, group).
+//   Forwards, block teams: a block per row, many on an SM, so that one's barriers are the others' time.
+//   All others walk down the rows on one set of columns, the coming rows on their way into shared
+//   memory, where each thread copies and reads its own vectors only: several rows in flight without a
+//   register or a barrier for them. Backwards the columns' weight gradients stay in registers over all
+//   rows and each block leaves one partial sum; a second kernel adds those in a fixed order.
 #include "../../include/ssd_mixer.h"
 #include "ssd_common.cuh"
 #include "ssd_layer_norm.h"
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(256) layer_norm_dw_kernel(const LayerNorm p, i
 // VB bytes of a row: the raw words, and how many elements they are.
 template <typename T, int VB>
 struct RowVec {
-    static constexpr int kN = VB / (int)sizeof(T), kW = VB / 4;
+    static constexpr int kN = VB / (int)sizeof(T), kW = VB / 4;   // elements, words
     uint32_t w[kW];
     __device__ __forceinline__ void load(const T* p)
     {
@@ -141,7 +142,7 @@ struct RowVec {
         else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
 };
-// kN parameters from column c (aligned to kN * 4 bytes, at most 16), or a constant.
+// N parameters from column c (aligned to 4 N bytes, at most 16), or a constant.
 template <int N>
 __device__ __forceinline__ void load_params(const float* p, int64_t c, float none, float* f)
 {
@@ -160,122 +161,45 @@ __device__ __forceinline__ void load_params(const float* p, int64_t c, float non
     }
 }
 
-// Sum over a team of TEAM lanes, or (TEAM = 0) over the block: red holds 32 values a call, and calls
-// alternate between two of them, so that one barrier a call is enough.
+// Sum over a team of TEAM lanes, or (TEAM = 0) over the block, in a fixed order. One barrier a call,
+// so successive calls take different `red` (32 values).
 template <int TEAM>
-__device__ __forceinline__ float team_sum(float v, float* red)
+__device__ __forceinline__ float team_sum1(float v, float* red)
 {
 #pragma unroll
     for (int o = (TEAM ? TEAM : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (TEAM == 0) {
-        const int warps = (blockDim.x + 31) >> 5, lane = threadIdx.x & 31;
+        const int lane = threadIdx.x & 31;
         if (lane == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = lane < warps ? red[lane] : 0.0f;
+        v = lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
     return v;
 }
+// Two sums at the price of one and a bit (an SM's warps share one shuffle unit): after the first
+// exchange the lower half of the team's lanes carries a, the upper half b. red: 64 floats.
 template <int TEAM>
-__device__ __forceinline__ float2 team_sum2(float2 v, float2* red)
+__device__ __forceinline__ float2 team_sum2(float a, float b, float* red)
 {
+    constexpr int H = (TEAM ? TEAM : 32) / 2;
+    const int lane = threadIdx.x & 31;
+    const bool up = (lane & H) != 0;
+    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, H);
 #pragma unroll
-    for (int o = (TEAM ? TEAM : 32) / 2; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
+    for (int o = H / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (TEAM == 0) {
-        const int warps = (blockDim.x + 31) >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) red[threadIdx.x >> 5] = v;
+        if ((lane & 15) == 0) red[(up ? 32 : 0) + (threadIdx.x >> 5)] = v;
         __syncthreads();
-        v = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
+        const int w = 2 * (lane & 15), warps = blockDim.x >> 5;
+        const float2 x = *reinterpret_cast<const float2*>(red + (up ? 32 : 0) + w);
+        v = (w < warps ? x.x : 0.0f) + (w + 1 < warps ? x.y : 0.0f);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        }
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
-    return v;
-}
-
-// TEAM lanes per group and R rows at a time (NV = 1), or the block on one group of one row (R = 1).
-template <typename T, int VB, int NV, int TEAM, int R>
-__global__ void __launch_bounds__(TEAM ? 256 : 1024) layer_norm_vec_kernel(const LayerNorm p)
-{
-    using V = RowVec<T, VB>;
-    static_assert(TEAM == 0 ? R == 1 : NV == 1, "lane teams hold one vector a lane, blocks one row");
-    __shared__ float red[2][32];
-    int64_t row0;
-    int g, t;
-    if constexpr (TEAM != 0) {
-        const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / TEAM;   // rows R to a team, groups fastest
-        g = (int)(id % p.groups);
-        row0 = id / p.groups * R;
-        t = threadIdx.x % TEAM;
-    } else {
-        g = (int)(blockIdx.x % p.groups);
-        row0 = blockIdx.x / p.groups;
-        t = threadIdx.x;
-    }
-    const int step = TEAM ? TEAM : blockDim.x, vecs = p.width / V::kN;
-    const float inv = 1.0f / (float)p.width;
-    const T* x = (const T*)p.x + (int64_t)g * p.width;
-    T* y = (T*)p.y + (int64_t)g * p.width;
-    V v[R][NV];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            v[r][i].zero();
-            if (t + i * step < vecs && row0 + r < p.rows) v[r][i].load(x + (row0 + r) * p.x_ld + (int64_t)(t + i * step) * V::kN);
-        }
-    float w[NV][V::kN], b[NV][V::kN];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (t + i * step < vecs && NV <= 2) {
-            load_params<V::kN>(p.weight, (int64_t)g * p.width + (t + i * step) * V::kN, 1.0f, w[i]);
-            load_params<V::kN>(p.bias, (int64_t)g * p.width + (t + i * step) * V::kN, 0.0f, b[i]);
-        }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < V::kN; ++e) s += v[r][i].at(e);
-        const float m = team_sum<TEAM>(s, red[0]) * inv;
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (t + i * step < vecs)
-#pragma unroll
-                for (int e = 0; e < V::kN; ++e) {
-                    const float d = v[r][i].at(e) - m;
-                    s = fmaf(d, d, s);
-                }
-        const float rs = 1.0f / sqrtf(team_sum<TEAM>(s, red[1]) * inv + p.eps);
-        if (row0 + r >= p.rows) continue;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (t + i * step < vecs) {
-                if constexpr (NV > 2) {      // many vectors: the parameters would not fit beside them
-                    load_params<V::kN>(p.weight, (int64_t)g * p.width + (t + i * step) * V::kN, 1.0f, w[i]);
-                    load_params<V::kN>(p.bias, (int64_t)g * p.width + (t + i * step) * V::kN, 0.0f, b[i]);
-                }
-                float f[V::kN];
-#pragma unroll
-                for (int e = 0; e < V::kN; ++e) f[e] = fmaf((v[r][i].at(e) - m) * rs, w[i][e], b[i][e]);
-                V o;
-                o.set(f);
-                o.store(y + (row0 + r) * p.y_ld + (int64_t)(t + i * step) * V::kN);
-            }
-        if (t == 0) {
-            const int64_t seg = (row0 + r) * p.groups + g;
-            if (p.mean) p.mean[seg] = m;
-            if (p.rstd) p.rstd[seg] = rs;
-        }
-    }
+    const float other = __shfl_xor_sync(0xffffffffu, v, H);
+    return up ? make_float2(other, v) : make_float2(v, other);
 }
 
 // VB bytes global -> shared, asynchronously; and all but the newest N groups of this thread's copies.
@@ -289,112 +213,245 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// dx, and this block's share of dweight and dbias. Lane teams: the block's columns are blockDim.x
-// vectors from blockIdx.x * blockDim.x; block teams: group blockIdx.x. Rows blockIdx.y, blockIdx.y +
-// gridDim.y, .. The coming rows wait in shared memory, where each thread copies and reads its own
-// vectors only: several rows deep without a register or a barrier for it (two rows ahead in registers
-// spilled, one row was not enough in flight).
-constexpr int ring_rows(int nv) { return nv == 1 ? 4 : 3; }   // 128 KB of 1024 threads, 192 KB of 512 with four vectors
+// The columns of a block and the ring of its rows: OPS operands (x, or x and dy), kRing rows deep.
+// Lane teams: the block's columns are blockDim.x vectors from blockIdx.x * blockDim.x; block teams:
+// group blockIdx.x. Rows blockIdx.y, blockIdx.y + gridDim.y, ..
+SSD_HD constexpr int ring_rows(int nv, int ops) { return nv == 4 && ops == 2 ? 3 : 4; }   // at most 192 KB a block
+template <typename T, int VB, int NV, int TEAM, int OPS>
+struct RowWalk {
+    using V = RowVec<T, VB>;
+    static constexpr int kRing = ring_rows(NV, OPS);
+    unsigned char* ring;
+    uint32_t ring0;
+    int step, tid, vecs, g, slot;
+    int64_t c0, row, stride, rows;
+    const T *x, *dy;            // this thread's first vector of the next row to fetch
+
+    __device__ __forceinline__ RowWalk(const LayerNorm& p, unsigned char* r)
+        : ring(r), ring0((uint32_t)__cvta_generic_to_shared(r)), step(blockDim.x), tid(threadIdx.x), slot(0), row(blockIdx.y),
+          stride(gridDim.y), rows(p.rows)
+    {
+        const int64_t C = p.channels();
+        c0 = TEAM ? (int64_t)blockIdx.x * blockDim.x * V::kN : (int64_t)blockIdx.x * p.width;
+        vecs = TEAM ? (int)((C - c0) / V::kN < step ? (C - c0) / V::kN : step) : p.width / V::kN;
+        g = TEAM ? (int)((c0 + (int64_t)(tid < vecs ? tid : 0) * V::kN) / p.width) : (int)blockIdx.x;
+        x = (const T*)p.x + row * p.x_ld + col(0);
+        if (OPS == 2) dy = (const T*)p.dy + row * p.dy_ld + col(0);
+#pragma unroll
+        for (int a = 0; a < kRing - 1; ++a) fetch(p, row + a * stride, a);
+    }
+    __device__ __forceinline__ bool in(int i) const { return tid + i * step < vecs; }
+    __device__ __forceinline__ int64_t col(int i) const { return c0 + (int64_t)(tid + i * step) * V::kN; }
+    __device__ __forceinline__ uint32_t at(int a, int o, int i) const
+    {
+        return (uint32_t)((((a * OPS + o) * NV + i) * step + tid) * VB);
+    }
+    __device__ __forceinline__ void fetch(const LayerNorm& p, int64_t r, int a)
+    {
+        if (r < rows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in(i)) {
+                    copy_async<VB>(ring0 + at(a, 0, i), x + i * step * V::kN);
+                    if (OPS == 2) copy_async<VB>(ring0 + at(a, 1, i), dy + i * step * V::kN);
+                }
+            x += stride * p.x_ld;
+            if (OPS == 2) dy += stride * p.dy_ld;
+        }
+        copy_commit();
+    }
+    // The present row's vectors (zeros past the columns), and on to the next row: the slot read one
+    // row ago takes the row kRing - 1 further on.
+    __device__ __forceinline__ void take(const LayerNorm& p, V (*v)[NV])
+    {
+        copy_wait<kRing - 2>();
+#pragma unroll
+        for (int o = 0; o < OPS; ++o)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                v[o][i].zero();
+                if (in(i)) v[o][i].load(reinterpret_cast<const T*>(ring + at(slot, o, i)));
+            }
+        fetch(p, row + (kRing - 1) * stride, slot == 0 ? kRing - 1 : slot - 1);
+        slot = slot == kRing - 1 ? 0 : slot + 1;
+    }
+};
+
+// Lane teams, down the rows.
+template <typename T, int VB, int TEAM>
+__global__ void __launch_bounds__(256) layer_norm_lanes_kernel(const LayerNorm p)
+{
+    using W = RowWalk<T, VB, 1, TEAM, 1>;
+    using V = typename W::V;
+    extern __shared__ __align__(16) unsigned char ring[];
+    W it(p, ring);
+    const float inv = 1.0f / (float)p.width;
+    float w[V::kN], b[V::kN];
+    load_params<V::kN>(it.in(0) ? p.weight : nullptr, it.col(0), 1.0f, w);
+    load_params<V::kN>(it.in(0) ? p.bias : nullptr, it.col(0), 0.0f, b);
+    for (; it.row < p.rows; it.row += it.stride) {
+        V v[1][1];
+        it.take(p, v);
+        float f[V::kN], s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V::kN; ++e) s += f[e] = v[0][0].at(e);
+        const float m = team_sum1<TEAM>(s, nullptr) * inv;
+        s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V::kN; ++e) {
+            f[e] -= m;
+            s = fmaf(f[e], f[e], s);
+        }
+        const float rs = 1.0f / sqrtf(team_sum1<TEAM>(s, nullptr) * inv + p.eps);
+        if (it.in(0)) {
+#pragma unroll
+            for (int e = 0; e < V::kN; ++e) f[e] = fmaf(f[e] * rs, w[e], b[e]);
+            V o;
+            o.set(f);
+            o.store((T*)p.y + it.row * p.y_ld + it.col(0));
+            if (it.tid % TEAM == 0) {
+                const int64_t seg = it.row * p.groups + it.g;
+                if (p.mean) p.mean[seg] = m;
+                if (p.rstd) p.rstd[seg] = rs;
+            }
+        }
+    }
+    copy_wait<0>();
+}
+
+// A block, or (TEAM = 32) each warp of it, per (row, group).
+template <typename T, int VB, int NV, int TEAM>
+__global__ void __launch_bounds__(TEAM ? 128 : (NV > 4 ? 512 : 1024)) layer_norm_block_kernel(const LayerNorm p)
+{
+    using V = RowVec<T, VB>;
+    __shared__ float red[2][32];
+    const int64_t seg = TEAM ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    if (TEAM && seg >= p.rows * p.groups) return;
+    const int t = TEAM ? threadIdx.x & 31 : threadIdx.x, step = TEAM ? 32 : blockDim.x, vecs = p.width / V::kN;
+    const int g = (int)(seg % p.groups);
+    const int64_t row = seg / p.groups, c0 = (int64_t)g * p.width + t * V::kN;
+    const T* x = (const T*)p.x + row * p.x_ld + c0;
+    const float inv = 1.0f / (float)p.width;
+    float f[NV][V::kN];
+    {
+        V v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            v[i].zero();
+            if (t + i * step < vecs) v[i].load(x + i * step * V::kN);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < V::kN; ++e) f[i][e] = v[i].at(e);
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < V::kN; ++e) s += f[i][e];
+    const float m = team_sum1<TEAM>(s, red[0]) * inv;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (t + i * step < vecs)
+#pragma unroll
+            for (int e = 0; e < V::kN; ++e) {
+                f[i][e] -= m;
+                s = fmaf(f[i][e], f[i][e], s);
+            }
+    const float rs = 1.0f / sqrtf(team_sum1<TEAM>(s, red[1]) * inv + p.eps);
+    T* y = (T*)p.y + row * p.y_ld + c0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (t + i * step < vecs) {
+            float w[V::kN], b[V::kN];
+            load_params<V::kN>(p.weight, c0 + i * step * V::kN, 1.0f, w);
+            load_params<V::kN>(p.bias, c0 + i * step * V::kN, 0.0f, b);
+#pragma unroll
+            for (int e = 0; e < V::kN; ++e) f[i][e] = fmaf(f[i][e] * rs, w[e], b[e]);
+            V o;
+            o.set(f[i]);
+            o.store(y + i * step * V::kN);
+        }
+    if (t == 0) {
+        if (p.mean) p.mean[seg] = m;
+        if (p.rstd) p.rstd[seg] = rs;
+    }
+}
+
+// dx = rs dy w + (A x + B), A = -rs rs mean(dh xh), B = -rs mean(dh) - m A: three operations an element.
 template <typename T, int VB, int NV, int TEAM>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) layer_norm_grad_kernel(const LayerNorm p)
 {
-    using V = RowVec<T, VB>;
-    constexpr int kRing = ring_rows(NV);
+    using W = RowWalk<T, VB, NV, TEAM, 2>;
+    using V = typename W::V;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ float2 red[2][32];
-    const int step = blockDim.x, tid = threadIdx.x;
+    __shared__ __align__(16) float red[2][64];
+    W it(p, ring);
     const int64_t C = p.channels();
-    const int64_t c0 = TEAM ? (int64_t)blockIdx.x * blockDim.x * V::kN : (int64_t)blockIdx.x * p.width;   // first column
-    const int vecs = TEAM ? (int)((C - c0) / V::kN < step ? (C - c0) / V::kN : step) : p.width / V::kN;
-    const int g = TEAM ? (int)((c0 + (int64_t)(tid < vecs ? tid : 0) * V::kN) / p.width) : (int)blockIdx.x;
     const float inv = 1.0f / (float)p.width;
-    const T* x = (const T*)p.x + c0;
-    const T* dy = (const T*)p.dy + c0;
-    T* dx = (T*)p.y + c0;
-    const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring);
-    // slot a, operand o, vector i of this thread
-    auto at = [&](int a, int o, int i) { return (uint32_t)((((a * 2 + o) * NV + i) * step + tid) * VB); };
-    auto fetch = [&](int64_t row, int a) {
-        if (row < p.rows) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * step < vecs) {
-                    copy_async<VB>(ring0 + at(a, 0, i), x + row * p.x_ld + (int64_t)(tid + i * step) * V::kN);
-                    copy_async<VB>(ring0 + at(a, 1, i), dy + row * p.dy_ld + (int64_t)(tid + i * step) * V::kN);
-                }
-        }
-        copy_commit();
-    };
     float dw[NV][V::kN], db[NV][V::kN], w[V::kN];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < V::kN; ++e) dw[i][e] = db[i][e] = 0.0f;
-    int64_t row = blockIdx.y;
-    const int64_t stride = gridDim.y;
-#pragma unroll
-    for (int a = 0; a < kRing - 1; ++a) fetch(row + a * stride, a);
-    if (NV == 1) load_params<V::kN>(tid < vecs ? p.weight : nullptr, c0 + tid * V::kN, 1.0f, w);
+    if (NV == 1) load_params<V::kN>(it.in(0) ? p.weight : nullptr, it.col(0), 1.0f, w);
+    const float *mp = p.mean + it.row * p.groups + it.g, *rp = p.rstd + it.row * p.groups + it.g;
+    const int64_t sstep = it.stride * p.groups;
     float m_next = 0.0f, r_next = 0.0f;
-    if (row < p.rows) {
-        m_next = p.mean[row * p.groups + g];
-        r_next = p.rstd[row * p.groups + g];
+    if (it.row < p.rows) {
+        m_next = *mp;
+        r_next = *rp;
     }
-    int slot = 0;
-    for (int k = 0; row < p.rows; row += stride, ++k) {
-        const float m = m_next, rs = r_next;
-        if (row + stride < p.rows) {
-            m_next = p.mean[(row + stride) * p.groups + g];
-            r_next = p.rstd[(row + stride) * p.groups + g];
+    T* dx = (T*)p.y + it.row * p.y_ld + it.col(0);
+    for (int k = 0; it.row < p.rows; it.row += it.stride, k ^= 1) {
+        const float rs = r_next, c = -m_next * rs, m = m_next;
+        if (it.row + it.stride < p.rows) {
+            m_next = *(mp += sstep);
+            r_next = *(rp += sstep);
         }
-        copy_wait<kRing - 2>();
-        V vx[NV], vd[NV];
-        float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            vx[i].zero();
-            vd[i].zero();
-            if (tid + i * step < vecs) {
-                vx[i].load(reinterpret_cast<const T*>(ring + at(slot, 0, i)));
-                vd[i].load(reinterpret_cast<const T*>(ring + at(slot, 1, i)));
-                if (NV > 1) load_params<V::kN>(p.weight, c0 + (tid + i * step) * V::kN, 1.0f, w);
-#pragma unroll
-                for (int e = 0; e < V::kN; ++e) {
-                    const float d = vd[i].at(e), xh = (vx[i].at(e) - m) * rs, dh = d * w[e];
-                    dw[i][e] = fmaf(d, xh, dw[i][e]);
-                    db[i][e] += d;
-                    s.x += dh;
-                    s.y = fmaf(dh, xh, s.y);
-                }
-            }
-        }
-        // this thread has read the slot that the row kRing - 1 further on goes to one row ago
-        fetch(row + (kRing - 1) * stride, slot == 0 ? kRing - 1 : slot - 1);
-        slot = slot == kRing - 1 ? 0 : slot + 1;
-        s = team_sum2<TEAM>(s, red[k & 1]);
-        const float s1 = s.x * inv, s2 = s.y * inv;
+        V v[2][NV];
+        it.take(p, v);
+        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (tid + i * step < vecs) {
-                if (NV > 1) load_params<V::kN>(p.weight, c0 + (tid + i * step) * V::kN, 1.0f, w);
+            if (it.in(i)) {
+                if (NV > 1) load_params<V::kN>(p.weight, it.col(i), 1.0f, w);
+#pragma unroll
+                for (int e = 0; e < V::kN; ++e) {
+                    const float d = v[1][i].at(e), xh = fmaf(v[0][i].at(e), rs, c), dh = d * w[e];
+                    dw[i][e] = fmaf(d, xh, dw[i][e]);
+                    db[i][e] += d;
+                    s1 += dh;
+                    s2 = fmaf(dh, xh, s2);
+                }
+            }
+        const float2 s = team_sum2<TEAM>(s1, s2, red[k]);
+        const float A = -rs * rs * (s.y * inv), B = fmaf(-m, A, -rs * (s.x * inv));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (it.in(i)) {
+                if (NV > 1) load_params<V::kN>(p.weight, it.col(i), 1.0f, w);
                 float f[V::kN];
 #pragma unroll
-                for (int e = 0; e < V::kN; ++e) f[e] = rs * (vd[i].at(e) * w[e] - s1 - (vx[i].at(e) - m) * rs * s2);
+                for (int e = 0; e < V::kN; ++e) f[e] = fmaf(v[1][i].at(e), rs * w[e], fmaf(v[0][i].at(e), A, B));
                 V o;
                 o.set(f);
-                o.store(dx + row * p.y_ld + (int64_t)(tid + i * step) * V::kN);
+                o.store(dx + i * it.step * V::kN);
             }
+        dx += it.stride * p.y_ld;
     }
     copy_wait<0>();
     if (!p.part) return;
-    float* part = p.part + (int64_t)blockIdx.y * 2 * C + c0;
+    float* part = p.part + (int64_t)blockIdx.y * 2 * C;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (tid + i * step < vecs)
+        if (it.in(i))
 #pragma unroll
             for (int e = 0; e < V::kN; ++e) {
-                part[(tid + i * step) * V::kN + e] = dw[i][e];
-                part[C + (tid + i * step) * V::kN + e] = db[i][e];
+                part[it.col(i) + e] = dw[i][e];
+                part[C + it.col(i) + e] = db[i][e];
             }
 }
 
@@ -437,79 +494,95 @@ int vector_bytes(const LayerNorm& p)
 bool lane_team(int vecs) { return vecs >= 2 && vecs <= 32 && (vecs & (vecs - 1)) == 0; }
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
-template <typename T, int VB>
-bool forward_vec(const LayerNorm& p, cudaStream_t st)
-{
-    const int vecs = p.width / RowVec<T, VB>::kN;
-    if (lane_team(vecs)) {
-        constexpr int R = 4;
-        const int64_t teams = (p.rows + R - 1) / R * p.groups;
-        const unsigned grid = (unsigned)((teams * vecs + 255) / 256);
-        switch (vecs) {
-        case 2: layer_norm_vec_kernel<T, VB, 1, 2, R><<<grid, 256, 0, st>>>(p); break;
-        case 4: layer_norm_vec_kernel<T, VB, 1, 4, R><<<grid, 256, 0, st>>>(p); break;
-        case 8: layer_norm_vec_kernel<T, VB, 1, 8, R><<<grid, 256, 0, st>>>(p); break;
-        case 16: layer_norm_vec_kernel<T, VB, 1, 16, R><<<grid, 256, 0, st>>>(p); break;
-        default: layer_norm_vec_kernel<T, VB, 1, 32, R><<<grid, 256, 0, st>>>(p); break;
-        }
-        return true;
-    }
-    if (vecs < 32 || vecs > 4096) return false;
-    const unsigned grid = (unsigned)(p.rows * p.groups);
-    if (vecs <= 256) layer_norm_vec_kernel<T, VB, 1, 0, 1><<<grid, round32(vecs), 0, st>>>(p);
-    else if (vecs <= 512) layer_norm_vec_kernel<T, VB, 2, 0, 1><<<grid, round32((vecs + 1) / 2), 0, st>>>(p);
-    else layer_norm_vec_kernel<T, VB, 4, 0, 1><<<grid, round32((vecs + 3) / 4), 0, st>>>(p);
-    return true;
-}
-
-// Blocks of the gradient kernel: threads, vectors a thread, blocks across the columns.
-struct GradShape {
-    int threads, nv, cols;
+// Blocks of the kernels that walk down the rows: threads, vectors a thread, blocks across the columns,
+// and blocks resident on an SM together (1024 threads of 64 registers, or 512 of 128).
+struct RowShape {
+    int threads, nv, cols, per_sm;
 };
-GradShape grad_shape(int groups, int width, int vec)
+RowShape row_shape(int groups, int width, int vec)
 {
     const int vecs = width / vec;
+    RowShape s{};
     if (lane_team(vecs)) {
         const int64_t all = (int64_t)groups * vecs;
-        const int th = all >= 512 ? 512 : round32(all);
-        return {th, 1, (int)((all + th - 1) / th)};
+        s.threads = all >= 256 ? 256 : round32(all);
+        s.nv = 1;
+        s.cols = (int)((all + s.threads - 1) / s.threads);
+    } else {
+        if (vecs < 1 || vecs > 2048) return s;
+        s.nv = vecs <= 1024 ? 1 : 4;
+        s.threads = round32((vecs + s.nv - 1) / s.nv);
+        s.cols = groups;
     }
-    if (vecs < 32 || vecs > 4096) return {0, 0, 0};
-    if (vecs <= 1024) return {round32(vecs), 1, groups};
-    if (vecs <= 2048) return {round32((vecs + 3) / 4), 4, groups};
-    return {0, 0, 0};
+    s.per_sm = (s.nv == 1 ? 1024 : 512) / s.threads;
+    s.per_sm = s.per_sm < 1 ? 1 : s.per_sm;
+    return s;
 }
+int64_t rows_at_a_time(const RowShape& s, int sms) { return ((int64_t)sms * s.per_sm + s.cols - 1) / s.cols; }
 
-template <typename T, int VB, int NV, int TEAM>
-cudaError_t launch_grad(const LayerNorm& p, const GradShape& s, int parts, cudaStream_t st)
+template <typename K>
+cudaError_t launch_rows(K kernel, const LayerNorm& p, const RowShape& s, int ops, int vb, int64_t rows, cudaStream_t st)
 {
-    const int smem = ring_rows(NV) * 2 * NV * s.threads * VB;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(layer_norm_grad_kernel<T, VB, NV, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    layer_norm_grad_kernel<T, VB, NV, TEAM><<<dim3((unsigned)s.cols, (unsigned)parts), s.threads, smem, st>>>(p);
+    const int smem = ring_rows(s.nv, ops) * ops * s.nv * s.threads * vb;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3((unsigned)s.cols, (unsigned)rows), s.threads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-// False: not a shape that the vector kernel takes.
+// False: not a shape that the vector kernels take.
+template <typename T, int VB>
+bool forward_vec(const LayerNorm& p, cudaStream_t st, cudaError_t* e)
+{
+    const int vecs = p.width / RowVec<T, VB>::kN;
+    if (lane_team(vecs)) {
+        const RowShape s = row_shape(p.groups, p.width, RowVec<T, VB>::kN);
+        int64_t rows = rows_at_a_time(s, device_sm_count());
+        rows = rows < p.rows ? rows : p.rows;
+        const auto go = [&](auto kernel) { *e = launch_rows(kernel, p, s, 1, VB, rows < 65535 ? rows : 65535, st); };
+        switch (vecs) {
+        case 2: go(layer_norm_lanes_kernel<T, VB, 2>); break;
+        case 4: go(layer_norm_lanes_kernel<T, VB, 4>); break;
+        case 8: go(layer_norm_lanes_kernel<T, VB, 8>); break;
+        case 16: go(layer_norm_lanes_kernel<T, VB, 16>); break;
+        default: go(layer_norm_lanes_kernel<T, VB, 32>); break;
+        }
+        return true;
+    }
+    const unsigned grid = (unsigned)(p.rows * p.groups), warps = (unsigned)((p.rows * p.groups + 3) / 4);
+    // Rows of up to 384 vectors: a warp each (58 against 80 us for 65536 x 1024 bf16, 89 against 109 for
+    // 32768 x 2688), but a block where there are too few of them to fill the device (9 against 11 us for
+    // 256 x 2688). Blocks hold 32 elements a thread: fewer, or the parameters beside them, was slower
+    // (16384 x 8192 bf16: 127 us, with 16 elements 183), more too (132).
+    constexpr int kNV = RowVec<T, VB>::kN >= 8 ? 4 : 8;
+    if (vecs <= 384 && p.rows * p.groups >= (int64_t)device_sm_count() * 8) {
+        if (vecs <= 64) layer_norm_block_kernel<T, VB, 2, 32><<<warps, 128, 0, st>>>(p);
+        else if (vecs <= 128) layer_norm_block_kernel<T, VB, 4, 32><<<warps, 128, 0, st>>>(p);
+        else if (vecs <= 256) layer_norm_block_kernel<T, VB, 8, 32><<<warps, 128, 0, st>>>(p);
+        else layer_norm_block_kernel<T, VB, 12, 32><<<warps, 128, 0, st>>>(p);
+    } else if (vecs <= 512) layer_norm_block_kernel<T, VB, 2, 0><<<grid, round32((vecs + 1) / 2), 0, st>>>(p);
+    else if (vecs <= 4096) layer_norm_block_kernel<T, VB, kNV, 0><<<grid, round32((vecs + kNV - 1) / kNV), 0, st>>>(p);
+    else return false;
+    *e = cudaGetLastError();
+    return true;
+}
 template <typename T, int VB>
 bool backward_vec(const LayerNorm& p, int parts, cudaStream_t st, cudaError_t* e)
 {
-    const GradShape s = grad_shape(p.groups, p.width, RowVec<T, VB>::kN);
+    const RowShape s = row_shape(p.groups, p.width, RowVec<T, VB>::kN);
     if (!s.threads) return false;
     const int vecs = p.width / RowVec<T, VB>::kN;
+    const auto go = [&](auto kernel) { *e = launch_rows(kernel, p, s, 2, VB, parts, st); };
     if (lane_team(vecs)) {
         switch (vecs) {
-        case 2: *e = launch_grad<T, VB, 1, 2>(p, s, parts, st); break;
-        case 4: *e = launch_grad<T, VB, 1, 4>(p, s, parts, st); break;
-        case 8: *e = launch_grad<T, VB, 1, 8>(p, s, parts, st); break;
-        case 16: *e = launch_grad<T, VB, 1, 16>(p, s, parts, st); break;
-        default: *e = launch_grad<T, VB, 1, 32>(p, s, parts, st); break;
+        case 2: go(layer_norm_grad_kernel<T, VB, 1, 2>); break;
+        case 4: go(layer_norm_grad_kernel<T, VB, 1, 4>); break;
+        case 8: go(layer_norm_grad_kernel<T, VB, 1, 8>); break;
+        case 16: go(layer_norm_grad_kernel<T, VB, 1, 16>); break;
+        default: go(layer_norm_grad_kernel<T, VB, 1, 32>); break;
         }
-    } else {
-        *e = s.nv == 1 ? launch_grad<T, VB, 1, 0>(p, s, parts, st) : launch_grad<T, VB, 4, 0>(p, s, parts, st);
-    }
+    } else if (s.nv == 1) go(layer_norm_grad_kernel<T, VB, 1, 0>);
+    else go(layer_norm_grad_kernel<T, VB, 4, 0>);
     return true;
 }
 
@@ -518,7 +591,8 @@ cudaError_t forward(const LayerNorm& p, cudaStream_t st)
 {
     LaunchScope ls("layer_norm", st);
     const int vb = vector_bytes<T>(p);
-    if (vb == 16 ? forward_vec<T, 16>(p, st) : vb == 8 && forward_vec<T, 8>(p, st)) return cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if (vb == 16 ? forward_vec<T, 16>(p, st, &e) : vb == 8 && forward_vec<T, 8>(p, st, &e)) return e;
     const int64_t segs = p.rows * p.groups;
     layer_norm_kernel<T><<<(unsigned)((segs + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(p);
     return cudaGetLastError();
@@ -551,18 +625,17 @@ cudaError_t backward(const LayerNorm& p, int parts, cudaStream_t st)
 
 }  // namespace
 
-// Rows a backward pass works on at a time: as many blocks as fit on the device at 64 registers a
-// thread (1024 threads an SM). The vector's width follows from addresses that are not known here, so
-// the larger of the two counts is kept.
+// Rows a backward pass works on at a time: as many blocks as are resident on the device. The vector's
+// width follows from addresses that are not known here, so the larger of the two counts is kept.
 int layer_norm_parts(int64_t rows, int groups, int width, int act, int sms)
 {
     int64_t parts = 64;
     for (int vb = 8; vb <= 16; vb += 8) {
         const int n = vb / (act == SSD_BF16 ? 2 : 4);
         if (width % n) continue;
-        const GradShape s = grad_shape(groups, width, n);
+        const RowShape s = row_shape(groups, width, n);
         if (!s.threads) continue;
-        const int64_t fit = (int64_t)sms * (1024 / s.threads > 1 ? 1024 / s.threads : 1) / s.cols;
+        const int64_t fit = rows_at_a_time(s, sms);
         parts = parts > fit ? parts : fit;
     }
     return (int)(rows < 1 ? 1 : (rows < parts ? rows : parts));
