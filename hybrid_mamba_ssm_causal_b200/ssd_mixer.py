@@ -607,7 +607,7 @@ def _rows_on(t, name: str, rows: int, width: int, dtype, dev):
     shape = t.shape
     if t.dim() < 1 or shape[-1] != width or t.numel() != rows * width:
         raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(shape)}")
-    if rows == 0:
+    if rows == 0 or t.is_contiguous():
         return t.data_ptr(), width
     if width > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: last dim must have unit stride")
@@ -648,32 +648,35 @@ def _device_of(t, name: str):
     return t.device
 
 
+# The handle of a device's current stream without a Stream object around it (3 us of a small call's 20).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """Makes the tensors' device current and, where a stream is given, that stream too (so that what
-    the call allocates belongs to it). ``.ptr`` is the stream's handle."""
-    __slots__ = ("dev", "stream", "ctx", "ptr")
+    the call allocates belongs to it). Yields the stream's handle."""
+    __slots__ = ("dev", "stream", "ctx")
 
     def __init__(self, dev, stream):
-        self.dev, self.stream, self.ctx = dev, stream, []
+        self.dev, self.stream, self.ctx = dev, stream, None
 
     def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            c = torch.cuda.device(self.dev)
-            c.__enter__()
-            self.ctx.append(c)
-        if self.stream is not None:
-            s = self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-                _stream(self.stream), device=self.dev)
-            if s.device != self.dev:
-                self.__exit__(None, None, None)
-                raise ValueError(f"the stream is on {s.device}, the tensors on {self.dev}")
-            c = torch.cuda.stream(s)
-            c.__enter__()
-            self.ctx.append(c)
-            self.ptr = s.cuda_stream
-        else:
-            self.ptr = torch.cuda.current_stream().cuda_stream
-        return self
+        dev, stream = self.dev, self.stream
+        if stream is None and torch.cuda.current_device() == dev.index:
+            return _raw_stream(dev.index)
+        self.ctx = [torch.cuda.device(dev)]
+        self.ctx[0].__enter__()
+        if stream is None:
+            return _raw_stream(dev.index)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+        if stream.device != dev:
+            self.__exit__(None, None, None)
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.ctx.append(torch.cuda.stream(stream))
+        self.ctx[1].__enter__()
+        return stream.cuda_stream
 
     def __exit__(self, *exc):
         while self.ctx:
@@ -730,15 +733,15 @@ def linear_prefill(dims: LinearDims, q, k, v, log_decay, init_state=None, worksp
     lib = load_library()
     with _On(dev, stream) as on:
         if out is None:
-            o = torch.empty(b, L, H * dims.dv, dtype=dims.torch_dtype, device=dev)
-            fs = torch.empty(sshape, dtype=torch.float32, device=dev)
+            o = q.new_empty((b, L, H * dims.dv))
+            fs = log_decay.new_empty(sshape)
         else:
             o, fs = out
         po = _rows_on(o, "o", b * L, H * dims.dv, dims.torch_dtype, dev)
         pf = _whole(fs, "final_state", sshape, torch.float32, dev)
         pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
                                 lib.ssd_mixer_linear_prefill_workspace_size(ctypes.byref(cd)), "linear_prefill", dev)
-        st = lib.ssd_mixer_linear_prefill(ctypes.byref(cd), *rows, pd, pi, *po, pf, pw, nw, on.ptr)
+        st = lib.ssd_mixer_linear_prefill(ctypes.byref(cd), *rows, pd, pi, *po, pf, pw, nw, on)
     _check(st, "ssd_mixer_linear_prefill")
     return o, fs
 
@@ -761,13 +764,13 @@ def linear_prefill_varlen(dims: LinearDims, cu_seqlens, slot_idx, has_init, q, k
     lib = load_library()
     with _On(dev, stream) as on:
         if o is None:
-            o = torch.empty(T, H * dims.dv, dtype=dims.torch_dtype, device=dev)
+            o = q.new_empty((T, H * dims.dv))
         po = _rows_on(o, "o", T, H * dims.dv, dims.torch_dtype, dev)
         pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
                                 lib.ssd_mixer_linear_prefill_varlen_workspace_size(ctypes.byref(cd)),
                                 "linear_prefill_varlen", dev)
         st = lib.ssd_mixer_linear_prefill_varlen(ctypes.byref(cd), pcu, psl, phi, *rows, pd, ps, nslots, *po, pw, nw,
-                                                 on.ptr)
+                                                 on)
     _check(st, "ssd_mixer_linear_prefill_varlen")
     return o
 
@@ -785,9 +788,9 @@ def linear_decode_step(dims: LinearDims, q, k, v, log_decay, state, slot_idx=Non
     ps = _whole(state, "state", (nslots, H, dims.dv, dims.dk), torch.float32, dev)
     with _On(dev, stream) as on:
         if o is None:
-            o = torch.empty(b, H * dims.dv, dtype=dims.torch_dtype, device=dev)
+            o = q.new_empty((b, H * dims.dv))
         po = _rows_on(o, "o", b, H * dims.dv, dims.torch_dtype, dev)
-        st = load_library().ssd_mixer_linear_decode_step(ctypes.byref(cd), *rows, pd, ps, nslots, psl, *po, on.ptr)
+        st = load_library().ssd_mixer_linear_decode_step(ctypes.byref(cd), *rows, pd, ps, nslots, psl, *po, on)
     _check(st, "ssd_mixer_linear_decode_step")
     return o
 
@@ -807,16 +810,15 @@ def linear_backward(dims: LinearDims, q, k, v, log_decay, do, init_state=None, d
     pdf = _whole(dfinal_state, "dfinal_state", sshape, torch.float32, dev)
     lib = load_library()
     with _On(dev, stream) as on:
-        g = {"q": torch.empty(b, L, H * dims.dk, dtype=a, device=dev), "k": torch.empty(b, L, G * dims.dk, dtype=a, device=dev),
-             "v": torch.empty(b, L, G * dims.dv, dtype=a, device=dev),
-             "init_state": torch.empty(sshape, dtype=torch.float32, device=dev)}
+        g = {"q": q.new_empty((b, L, H * dims.dk)), "k": q.new_empty((b, L, G * dims.dk)),
+             "v": q.new_empty((b, L, G * dims.dv)), "init_state": log_decay.new_empty(sshape)}
         outs = []
         for n, w in (("q", H * dims.dk), ("k", G * dims.dk), ("v", G * dims.dv)):
             outs += [g[n].data_ptr(), w]
         pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
                                 lib.ssd_mixer_linear_backward_workspace_size(ctypes.byref(cd)), "linear_backward", dev)
         st = lib.ssd_mixer_linear_backward(ctypes.byref(cd), *rows, pd, pi, *pdo, pdf, *outs, g["init_state"].data_ptr(),
-                                           pw, nw, on.ptr)
+                                           pw, nw, on)
     _check(st, "ssd_mixer_linear_backward")
     return g
 
@@ -840,14 +842,15 @@ def layer_norm(x, weight=None, bias=None, groups: int = 1, eps: float = 1e-5, ou
     pw = _whole(weight, "weight", (C,), torch.float32, dev)
     pb = _whole(bias, "bias", (C,), torch.float32, dev)
     with _On(dev, stream) as on:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        y = x.new_empty(x.shape) if out is None else out
         py = _rows_on(y, "out", rows, C, x.dtype, dev)
-        stats = torch.empty((2, *x.shape[:-1], groups), dtype=torch.float32, device=dev)
+        stats = x.new_empty((2, *x.shape[:-1], groups), dtype=torch.float32)
         pm = stats.data_ptr()
         st = load_library().ssd_mixer_layer_norm(rows, groups, width, eps, act, *px, pw, pb, *py, pm,
-                                                 pm + 4 * rows * groups, on.ptr)
+                                                 pm + 4 * rows * groups, on)
     _check(st, "ssd_mixer_layer_norm")
-    return y, stats[0], stats[1]
+    mean, rstd = stats.unbind(0)
+    return y, mean, rstd
 
 
 def ssd_mixer_layer_norm_backward_workspace_size(rows: int, groups: int, width: int, act: str) -> int:
@@ -865,13 +868,14 @@ def layer_norm_backward(dy, x, weight, mean, rstd, groups: int = 1, workspace=No
     pm, pr = _whole(mean, "mean", sshape, torch.float32, dev), _whole(rstd, "rstd", sshape, torch.float32, dev)
     lib = load_library()
     with _On(dev, stream) as on:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        dpar = torch.empty(2, C, dtype=torch.float32, device=dev)
+        dx = x.new_empty(x.shape)
+        dpar = x.new_empty((2, C), dtype=torch.float32)
         pp = dpar.data_ptr()
         pws, nws, ws = _workspace(workspace, 0 if workspace is not None else
                                   lib.ssd_mixer_layer_norm_backward_workspace_size(rows, groups, width, act),
                                   "layer_norm_backward", dev)
         st = lib.ssd_mixer_layer_norm_backward(rows, groups, width, act, *pdy, *px, pw, pm, pr, dx.data_ptr(), C, pp,
-                                               pp + 4 * C, pws, nws, on.ptr)
+                                               pp + 4 * C, pws, nws, on)
     _check(st, "ssd_mixer_layer_norm_backward")
-    return dx, dpar[0], dpar[1]
+    dweight, dbias = dpar.unbind(0)
+    return dx, dweight, dbias
