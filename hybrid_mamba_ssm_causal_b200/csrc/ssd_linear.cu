@@ -377,13 +377,14 @@ cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStr
 }
 
 // Splitting rows into segments fills SMs that whole rows would leave idle, at the price of a pass over
-// k and v (and a kernel that joins the states) before the main one. Times in units of one block of 128
-// tokens of the main pass: a CTA's start costs about one and a half, a block of the states' pass 0.6,
-// the joining kernel and two more launches about 3. The tensor-core scan runs one CTA per SM, the
-// CUDA-core one two or more.
+// k and v before the main one and of the segments' states. Times in units of one block of 128 tokens
+// of the main pass. Tensor cores: a CTA per SM takes segment after segment, each some 0.8 to start; a
+// block of the states' pass is 0.5; the two more launches 2, and every segment's state goes through
+// memory four times. CUDA cores: two CTAs per SM or more, one segment each.
 int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms)
 {
     const int64_t rows = b * H * nscans, slots = tc ? sms : 2 * sms;
+    const double start = tc ? 0.8 : 1.5, states = tc ? 0.5 : 0.6, join = tc ? 2.0 : 3.0, each = tc ? 0.01 : 0.02;
     const int64_t blocks = ((packed ? T : L) + 127) / 128;
     if (blocks <= 1 || b == 0) return 256;                 // nothing to split: longer than any row
     // a packed row's length is not known here; they are taken as equal, and each may end in part of a segment
@@ -394,8 +395,9 @@ int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool pac
         const int64_t seg = (per_row + nseg - 1) / nseg;
         if (best_seg && seg == best_seg) continue;
         const int64_t n = packed ? (int64_t)H * nscans * (blocks / seg + (b + 1) / 2) : rows * ((per_row + seg - 1) / seg);
-        double cost = (double)((n + slots - 1) / slots) * (seg + 1.5);
-        if (seg < per_row) cost += (double)((n - rows > 0 ? n - rows + slots - 1 : slots) / slots) * (0.6 * seg + 1.5) + 3.0;
+        double cost = (double)((n + slots - 1) / slots) * (seg + start);
+        if (seg < per_row)
+            cost += (double)((n - rows > 0 ? n - rows + slots - 1 : slots) / slots) * (states * seg + start) + join + each * (double)n * 148.0 / (double)sms;
         if (!best_seg || cost < best) {
             best = cost;
             best_seg = seg;

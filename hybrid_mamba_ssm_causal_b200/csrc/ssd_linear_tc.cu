@@ -15,15 +15,21 @@
 // that the state is as exact as its fp32 sums; P and the operand copy of S are rounded to bf16 once,
 // which is as much as the rounding of o itself.
 //
-// Four warpgroups, so that the next block's w V and scores are under way while this one's state and
-// outputs are finished; registers are moved to the two that hold tiles (setmaxnreg):
+// One CTA per SM, which takes segment after segment; a row that is cut into several has their own
+// states computed first (the same kernel without q and o) and joined by a small kernel between.
+// Four warpgroups, so that the next block's (and the next segment's) loads, w V and scores are under
+// way while this one's state and outputs are finished; registers are moved to the two that hold tiles
+// (setmaxnreg):
 //   0  outputs, a row i each: scores -> P, then o = c l^{i+1} inter + intra, staged over the block's
 //      own tiles for a TMA store
 //   1  state, a row d each: S += U, and its operand copy
 //   2  w V: V's tile transposed by ldmatrix, times w, into TMEM, 32 tokens at a time in two slots
-//   3  one warp each for TMA loads, every MMA, and the stores
+//   3  one warp each for TMA loads, every MMA, the stores, and the list of segments: where each lies
+//      and its head's powers of l, one segment ahead
 // TMEM columns: QK and, over its first half, P; one output tile (inter is read out before intra
-// overwrites it); U; the two slots of w V.
+// overwrites it); U; the two slots of w V. The loops are kept rolled where registers allow: the four
+// warpgroups' code competes for the instruction cache. Nothing may spill: beside 227 KB of shared
+// memory the L1 has some 16 KB left.
 //
 // No decay factor is ever above 1: off the diagonal 32 x 32 tiles, l^{i-j} = l^{i-j0-31} l^{31-(j-j0)}.
 #include <cuda.h>
@@ -52,20 +58,35 @@ constexpr int kSub = 32;                 // tokens of one slot of w V
 constexpr uint32_t kSlotCols = 64;       // its TMEM columns: three terms of 16, and 16 unused
 // Registers per thread of the four warpgroups; they share what the launch gave them (512 x 128).
 constexpr int kRegsOut = 208, kRegsState = 184, kRegsV = 72, kRegsCtl = 48;
+constexpr int kRegsStateOnly = 208;      // where warpgroup 0 makes w V too
 static_assert(kRegsOut + kRegsState + kRegsV + kRegsCtl <= 4 * 128, "more registers than the launch's");
+static_assert(2 * kRegsV + kRegsStateOnly + kRegsCtl <= 4 * 128, "more registers than the launch's");
 
 template <int DK, int DV, bool STATES>
 struct Cfg {
     static constexpr uint32_t kQ = STATES ? 0 : kAtom * (DK / 64), kK = kAtom * (DK / 64), kV = kAtom * (DV / 64);
     static constexpr uint32_t kStage = kQ + kK + kV;
-    static constexpr uint32_t kS = STATES ? 0 : DV * DK * 2;
-    static constexpr uint32_t kTail = 2560;      // decay tables, barriers
+    static constexpr uint32_t kS = DV * DK * 2;  // operand copy of S; staging of whole states
+    static constexpr uint32_t kTail = 2048;      // the segments' powers and places, barriers
     static constexpr int kFit = (int)((kSmemMax - kS - kTail) / kStage);
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static_assert(kStages >= 2, "two stages");
-    static constexpr uint32_t kOffS = kStages * kStage, kOffTab = kOffS + kS, kOffBar = kOffTab + 1712;
-    static constexpr uint32_t kSmem = kOffTab + kTail;
+    static constexpr uint32_t kOffS = kStages * kStage, kOffWork = kOffS + kS, kOffBar = kOffWork + 2 * 720;
+    static constexpr uint32_t kSmem = kOffWork + kTail;
 };
+
+// One segment of one scan, as the list warp leaves it for the others.
+struct Work {
+    float tab[132];      // l^0 .. l^128
+    float wtab[32];      // l^{31-x} (backwards l^x)
+    float log_l;
+    int n;               // tokens; -1: the list has ended
+    int row0, scan, head, slot;
+    int flags;
+    int item;            // seg_states index
+};
+enum : int { kFirstInit = 1, kSplit = 2, kFinal = 4 };   // from an initial state; one of several segments; the scan's last
+static_assert(sizeof(Work) <= 720, "room for two");
 
 struct ScanMaps {
     CUtensorMap q, k, v, o;
@@ -95,6 +116,16 @@ __device__ __forceinline__ bool elect_one()
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
     return p != 0;
 }
+// Barrier `id` of n threads; true if `p` is in all of them.
+__device__ __forceinline__ bool named_all(int id, int n, bool p)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.cta.red.and.pred b, %2, %3, a;\n\tselp.u32 %0, 1, 0, b;\n\t}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)p), "r"(id), "r"(n)
+                 : "memory");
+    return r != 0;
+}
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -117,32 +148,67 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  : "memory");
 }
 
+// A warp's 32 rows of a state: row-major fp32 in global memory, a row a lane in registers, through 32
+// rows of DK * 2 bytes of shared memory (half of the columns at a time, chunks of 16 bytes permuted by
+// the row) so that the global side is coalesced.
+template <int DK>
+__device__ __forceinline__ void load_state(const float* p, unsigned char* buf, int lane, float* S)
+{
+    constexpr int kC = DK / 8;                    // 16-byte chunks of half a row
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll 4
+        for (int x = lane; x < 32 * kC; x += 32) {
+            const int r = x / kC, ch = x % kC;
+            const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)r * DK + half * (DK / 2) + ch * 4);
+            *reinterpret_cast<float4*>(buf + r * (DK * 2) + ((ch ^ (r & 7)) << 4)) = v;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < kC; ++ch) {
+            const float4 v = *reinterpret_cast<const float4*>(buf + lane * (DK * 2) + ((ch ^ (lane & 7)) << 4));
+            float* o = S + half * (DK / 2) + ch * 4;
+            o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+        }
+        __syncwarp();
+    }
+}
+template <int DK>
+__device__ __forceinline__ void store_state(float* p, unsigned char* buf, int lane, const float* S)
+{
+    constexpr int kC = DK / 8;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int ch = 0; ch < kC; ++ch) {
+            const float* v = S + half * (DK / 2) + ch * 4;
+            *reinterpret_cast<float4*>(buf + lane * (DK * 2) + ((ch ^ (lane & 7)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int x = lane; x < 32 * kC; x += 32) {
+            const int r = x / kC, ch = x % kC;
+            *reinterpret_cast<float4*>(p + (int64_t)r * DK + half * (DK / 2) + ch * 4) =
+                *reinterpret_cast<const float4*>(buf + r * (DK * 2) + ((ch ^ (r & 7)) << 4));
+        }
+        __syncwarp();
+    }
+}
+
 template <int DK, int DV, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps)
 {
     using C = Cfg<DK, DV, STATES>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const LinearCall& c = a.c;
-    const int z = blockIdx.x % a.nscans;
-    const int h = (int)((blockIdx.x / a.nscans) % c.H);
-    const int64_t item = blockIdx.x / a.nscans / c.H;
-    const LinearScan& s = a.s[z];
-    LinearItem it;
-    if (!linear_item(c, item, &it)) return;
-    const bool rev = s.reverse;
-    const bool last = rev ? it.seg == 0 : it.seg == it.nseg - 1;
-    if (STATES && last) return;
-
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // the same in a warp, as the compiler sees
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the compiler sees
     const uint32_t sb = smem_u32(smem);
     if (sb & 1023u) {
         if (tid == 0) set_device_status(c.status, kDevSmemMisaligned);
         return;
     }
-    float* tab = reinterpret_cast<float*>(smem + C::kOffTab);      // l^0 .. l^128
-    float* ptab = tab + 132;                                       // the same times c u
-    float* wtab = ptab + 132;                                      // l^{31-x} (backwards l^x), x = 0 .. 31
-    float* vtab = wtab + 32;                                       // u l^{127-j} (backwards u l^{j+1}), j = 0 .. 127
+    Work* works = reinterpret_cast<Work*>(smem + C::kOffWork);
+    static_assert(C::kOffBar >= C::kOffWork + 2 * sizeof(Work) && C::kOffBar % 8 == 0, "work slots");
     const uint32_t bar0 = sb + C::kOffBar;
     auto q_full = [&](int i) { return bar0 + 8 * i; };
     auto q_empty = [&](int i) { return bar0 + 32 + 8 * i; };
@@ -150,15 +216,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     auto kv_empty = [&](int i) { return bar0 + 96 + 8 * i; };
     auto v_ready = [&](int i) { return bar0 + 128 + 8 * i; };
     auto v_free = [&](int i) { return bar0 + 144 + 8 * i; };
-    const uint32_t qk_done = bar0 + 160, p_ready = bar0 + 168, inter_done = bar0 + 176, inter_read = bar0 + 184,
-                   intra_done = bar0 + 192, o_free = bar0 + 200, o_staged = bar0 + 208, u_done = bar0 + 216,
-                   u_free = bar0 + 224, s_ready = bar0 + 232;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 240);
-    static_assert(C::kOffBar + 244 <= C::kSmem && C::kOffBar % 8 == 0 && C::kOffBar >= C::kOffTab + 424 * 4, "tail");
-
-    const int nb = (int)((it.n + kB - 1) / kB);
-    auto block = [&](int i) { return rev ? nb - 1 - i : i; };
-    auto tokens = [&](int b) { return it.n - (int64_t)b * kB < kB ? (int)(it.n - (int64_t)b * kB) : kB; };
+    auto w_full = [&](int i) { return bar0 + 160 + 8 * i; };
+    auto w_empty = [&](int i) { return bar0 + 176 + 8 * i; };
+    const uint32_t qk_done = bar0 + 192, p_ready = bar0 + 200, inter_done = bar0 + 208, inter_read = bar0 + 216,
+                   intra_done = bar0 + 224, o_free = bar0 + 232, o_staged = bar0 + 240, u_done = bar0 + 248,
+                   u_free = bar0 + 256, s_ready = bar0 + 264;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 272);
+    static_assert(C::kOffBar + 276 <= C::kSmem, "barriers");
+    constexpr int kReaders = STATES ? 14 : 15;   // warps that read a work slot
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -167,6 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(kv_full(i), 1);
             mbar_init(kv_empty(i), 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(v_ready(i), 128);
+            mbar_init(v_free(i), 1);
+            mbar_init(w_full(i), 1);
+            mbar_init(w_empty(i), kReaders);
+        }
         mbar_init(qk_done, 1);
         mbar_init(p_ready, 128);
         mbar_init(inter_done, 1);
@@ -174,37 +245,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         mbar_init(intra_done, 1);
         mbar_init(o_free, 128);
         mbar_init(o_staged, 128);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(v_ready(i), 128);
-            mbar_init(v_free(i), 1);
-        }
         mbar_init(u_done, 1);
         mbar_init(u_free, 128);
         mbar_init(s_ready, 128);
         fence_mbar_init();
-    }
-    const double g = (double)linear_log_decay(c.log_decay, h);
-    if (tid <= kB) {
-        const double p = exp(g * tid);
-        tab[tid] = (float)p;
-        ptab[tid] = (float)(p * s.out_scale * s.u_scale);
-    } else if (tid >= 256 && tid < 288) {
-        wtab[tid - 256] = (float)exp(g * (rev ? tid - 256 : 287 - tid));
-    } else if (tid >= 384) {
-        vtab[tid - 384] = (float)(exp(g * (rev ? tid - 383 : 511 - tid)) * s.u_scale);
     }
     if (warp == 13) tmem_alloc(smem_u32(tmem_slot), 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    // o is staged over Q's tiles; k's and v's are free as soon as the block's MMAs are done, unless o
-    // is larger than q
-    const bool kv_early = STATES || (DV <= DK && !s.o_f32);
     bool ok = true;
     auto wait = [&](uint32_t bar, int n) {   // the barrier's n-th completion (from 0)
         if (ok && !mbar_wait_bounded(bar, (uint32_t)(n & 1), kWait)) ok = false;
     };
+    // The k-th segment of this CTA; nullptr: there are no more, or a wait gave up, in which case all
+    // the warps that meet at named barriers (`group` threads at barrier `id`) leave together.
+    auto open = [&](int k, int id, int group) -> const Work* {
+        wait(w_full(k & 1), k >> 1);
+        ok = group > 32 ? named_all(id, group, ok) : __all_sync(0xffffffffu, ok);
+        const Work* w = works + (k & 1);
+        return ok && w->n >= 0 ? w : nullptr;
+    };
+    auto close = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(w_empty(k & 1));
+    };
+    // Blocks of a segment in scan order: block x of it, and that block's tokens.
+    auto block = [&](bool rev, int nb, int x) { return rev ? nb - 1 - x : x; };
+    auto tokens = [&](int n, int b) { return min(n - b * kB, kB); };
 
     if (STATES ? warp < 4 || (warp >= 8 && warp < 12) : warp >= 8 && warp < 12) {
         // ------------------------------------------------------------------ w V
@@ -222,71 +291,82 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             for (uint32_t x = 0; x < 2 * kSlotCols; x += 16) tmem_st16(lanes + x, zero);
             tmem_wait_st();
         }
-        for (int i = 0; i < nb; ++i) {
-            const int st = i % C::kStages;
-            const int n = tokens(block(i));
-            const uint32_t ok_off = (uint32_t)st * C::kStage + C::kQ, ov_off = ok_off + C::kK;
-            wait(kv_full(st), i / C::kStages);
-            if (n < kB && first == 0) {   // rows behind the sequence: whatever they hold must not meet a zero weight
-                for (int id = tid & 127; id < (kB - n) * 8; id += 128) {
-                    const int rr = n + (id >> 3), ch = (id & 7) << 4;
+        int i = 0;                                                 // blocks so far
+        for (int k = 0;; ++k) {
+            const Work* wk = open(k, STATES ? 3 : 2, STATES ? 256 : 128);
+            if (!wk) break;
+            const bool rev = a.s[wk->scan].reverse;
+            const float us = a.s[wk->scan].u_scale;
+            const int nall = wk->n, nb = (nall + kB - 1) / kB;
+            for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                const int st = i % C::kStages;
+                const int n = tokens(nall, block(rev, nb, x0));
+                const uint32_t k_off = (uint32_t)st * C::kStage + C::kQ, v_off = k_off + C::kK;
+                wait(kv_full(st), i / C::kStages);
+                if (n < kB && first == 0) {   // rows behind the sequence: whatever they hold must not meet a zero weight
+                    for (int id = tid & 127; id < (kB - n) * 8; id += 128) {
+                        const int rr = n + (id >> 3), ch = (id & 7) << 4;
 #pragma unroll
-                    for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(smem + ok_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
+                        for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(smem + k_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int x = 0; x < DV / 64; ++x) *reinterpret_cast<uint4*>(smem + ov_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
+                        for (int x = 0; x < DV / 64; ++x) *reinterpret_cast<uint4*>(smem + v_off + x * kAtom + rr * 128 + ch) = make_uint4(0, 0, 0, 0);
+                    }
+                    named_sync(2, 128);
+                    fence_async_smem();
                 }
-                named_sync(2, 128);
-                fence_async_smem();
-            }
-            if (n < kB && step == 2) named_sync(3, 256);
+                if (n < kB && step == 2) named_sync(3, 256);
 #pragma unroll 1
-            for (int u = first; u < kB / kSub; u += step) {
-                const int k = i * (kB / kSub) + u;
-                if (k >= 2) wait(v_free(k & 1), (k >> 1) - 1);
-                fence_after_sync();
-                if (mine) {
-                    // thread t's tokens of 8-token group x: j0 + 8 x, and the next. A short block is the
-                    // end of a row: forwards its weights are the last n. Rows behind it are zeros by
-                    // now, whatever weight they meet.
-                    const int j0 = u * kSub + 2 * (lane & 3) + (rev ? 0 : kB - n);
-                    float2 w[4];
+                for (int u = first; u < kB / kSub; u += step) {
+                    const int kk = i * (kB / kSub) + u;
+                    if (kk >= 2) wait(v_free(kk & 1), (kk >> 1) - 1);
+                    fence_after_sync();
+                    if (mine) {
+                        // thread t's tokens of 8-token group x: j0 + 8 x, and the next. A short block ends a
+                        // row; rows behind it are zeros by now, whatever weight they meet.
+                        const int j0 = u * kSub + 2 * (lane & 3);
+                        float2 w[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] = make_float2(vtab[min(j0 + 8 * x, kB - 1)], vtab[min(j0 + 8 * x + 1, kB - 1)]);
-                    // addresses: matrix m = lane / 8 is token group m, its row lane % 8 a token
-                    const uint32_t row = (uint32_t)(u * kSub + lane);
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {          // 16 rows d
-                        uint32_t raw[2][4], a0[8], a1[8], a2[8];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t ch = (uint32_t)(q * 4 + half * 2 + y);     // 8-column group of d
-                            ldmatrix_x4_trans(sb + ov_off + (ch >> 3) * kAtom + row * 128 + (((ch & 7) ^ (row & 7)) << 4), raw[y]);
+                        for (int x = 0; x < 4; ++x) {
+                            const int j = j0 + 8 * x, e = rev ? j + 1 : n - 1 - j, e1 = rev ? j + 2 : n - 2 - j;
+                            w[x] = make_float2(us * wk->tab[max(e, 0)], us * wk->tab[max(e1, 0)]);
                         }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
+                        // addresses: matrix m = lane / 8 is token group m, its row lane % 8 a token
+                        const uint32_t row = (uint32_t)(u * kSub + lane);
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {          // 16 rows d
+                            uint32_t raw[2][4], a0[8], a1[8], a2[8];
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                const float2 v = bf2_to_f2(raw[y][x]);
-                                float2 t = mul2(v, w[x]);
-                                const uint32_t h0 = pack_f2(t);
-                                float2 b0 = bf2_to_f2(h0);
-                                t = make_float2(t.x - b0.x, t.y - b0.y);
-                                const uint32_t h1 = pack_f2(t);
-                                b0 = bf2_to_f2(h1);
-                                a0[2 * x + y] = h0;
-                                a1[2 * x + y] = h1;
-                                a2[2 * x + y] = pack_bf16x2(t.x - b0.x, t.y - b0.y);
+                                const uint32_t ch = (uint32_t)(q * 4 + half * 2 + y);     // 8-column group of d
+                                ldmatrix_x4_trans(sb + v_off + (ch >> 3) * kAtom + row * 128 + (((ch & 7) ^ (row & 7)) << 4), raw[y]);
                             }
-                        const uint32_t at = lanes + ((uint32_t)(half * 16) << 16) + (uint32_t)(k & 1) * kSlotCols;
-                        tmem_st_16x128b_x4(at, a0);
-                        tmem_st_16x128b_x4(at + 16, a1);
-                        tmem_st_16x128b_x4(at + 32, a2);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const float2 v = bf2_to_f2(raw[y][x]);
+                                    float2 t = mul2(v, w[x]);
+                                    const uint32_t h0 = pack_f2(t);
+                                    float2 b0 = bf2_to_f2(h0);
+                                    t = make_float2(t.x - b0.x, t.y - b0.y);
+                                    const uint32_t h1 = pack_f2(t);
+                                    b0 = bf2_to_f2(h1);
+                                    a0[2 * x + y] = h0;
+                                    a1[2 * x + y] = h1;
+                                    a2[2 * x + y] = pack_bf16x2(t.x - b0.x, t.y - b0.y);
+                                }
+                            const uint32_t at = lanes + ((uint32_t)(half * 16) << 16) + (uint32_t)(kk & 1) * kSlotCols;
+                            tmem_st_16x128b_x4(at, a0);
+                            tmem_st_16x128b_x4(at + 16, a1);
+                            tmem_st_16x128b_x4(at + 32, a2);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
+                    fence_before_sync();
+                    mbar_arrive_local(v_ready(kk & 1));
                 }
-                fence_before_sync();
-                mbar_arrive_local(v_ready(k & 1));
             }
+            close(k);
         }
     } else if (!STATES && warp < 4) {
         // ------------------------------------------------------------------ scores and outputs
@@ -294,310 +374,401 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if constexpr (!STATES) {
             const int r = tid;                                     // row i of the block = TMEM lane
             const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-            const float out_scale = s.out_scale;
-            const bool o_f32 = s.o_f32;
-            for (int i = 0; i < nb; ++i) {
-                const int st = i % C::kStages;
-                const int b = block(i), n = tokens(b);
-                wait(qk_done, i);
-                fence_after_sync();
-                // 32 score columns at a time. The loops here are kept rolled where registers allow: four
-                // warpgroups' code competes for the instruction cache.
+            int i = 0;
+            for (int k = 0;; ++k) {
+                const Work* wk = open(k, 1, 128);
+                if (!wk) break;
+                const LinearScan& s = a.s[wk->scan];
+                const bool rev = s.reverse, o_f32 = s.o_f32;
+                const float out_scale = s.out_scale, ps = s.out_scale * s.u_scale;
+                const float* tab = wk->tab;
+                const int nall = wk->n, nb = (nall + kB - 1) / kB;
+                for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                    const int st = i % C::kStages;
+                    const int b = block(rev, nb, x0), n = tokens(nall, b);
+                    wait(qk_done, i);
+                    fence_after_sync();
 #pragma unroll 1
-                for (int m = 0; m < 4; ++m) {
-                    uint32_t p[16];
-                    if (rev ? m < warp : m > warp) {               // all outside the mask
+                    for (int m = 0; m < 4; ++m) {                  // 32 score columns at a time
+                        uint32_t p[16];
+                        if (rev ? m < warp : m > warp) {           // all outside the mask
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) p[x] = 0;
-                    } else {
-                        float a[32];
-                        tmem_ld32(lanes + kColP + 32 * m, a);
-                        tmem_wait_ld();
-                        if (m == warp) {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                const float t = a[x] * ptab[rev ? max(x - lane, 0) : max(lane - x, 0)];
-                                a[x] = (rev ? x >= lane : x <= lane) ? t : 0.0f;
-                            }
+                            for (int x = 0; x < 16; ++x) p[x] = 0;
                         } else {
-                            const float2 f = splat2(ptab[rev ? 32 * m - r : r - 32 * m - 31]);
+                            float v[32];
+                            tmem_ld32(lanes + kColP + 32 * m, v);
+                            tmem_wait_ld();
+                            if (m == warp) {
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const float4 t = reinterpret_cast<const float4*>(wtab)[x];
-                                const float2 t0 = mul2(mul2(f, make_float2(t.x, t.y)), make_float2(a[4 * x], a[4 * x + 1]));
-                                const float2 t1 = mul2(mul2(f, make_float2(t.z, t.w)), make_float2(a[4 * x + 2], a[4 * x + 3]));
-                                a[4 * x] = t0.x;
-                                a[4 * x + 1] = t0.y;
-                                a[4 * x + 2] = t1.x;
-                                a[4 * x + 3] = t1.y;
+                                for (int x = 0; x < 32; ++x) {
+                                    const float t = v[x] * (ps * tab[rev ? max(x - lane, 0) : max(lane - x, 0)]);
+                                    v[x] = (rev ? x >= lane : x <= lane) ? t : 0.0f;
+                                }
+                            } else {
+                                const float2 f = splat2(ps * tab[rev ? 32 * m - r : r - 32 * m - 31]);
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) {
+                                    const float4 t = reinterpret_cast<const float4*>(wk->wtab)[x];
+                                    const float2 t0 = mul2(mul2(f, make_float2(t.x, t.y)), make_float2(v[4 * x], v[4 * x + 1]));
+                                    const float2 t1 = mul2(mul2(f, make_float2(t.z, t.w)), make_float2(v[4 * x + 2], v[4 * x + 3]));
+                                    v[4 * x] = t0.x;
+                                    v[4 * x + 1] = t0.y;
+                                    v[4 * x + 2] = t1.x;
+                                    v[4 * x + 3] = t1.y;
+                                }
                             }
-                        }
-                        const int left = n - 32 * m;               // columns that are tokens
-                        if (left < 32) {
+                            const int left = n - 32 * m;           // columns that are tokens
+                            if (left < 32) {
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) a[x] = x < left ? a[x] : 0.0f;
-                        }
+                                for (int x = 0; x < 32; ++x) v[x] = x < left ? v[x] : 0.0f;
+                            }
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(a[2 * x], a[2 * x + 1]);
+                            for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+                        }
+                        tmem_st16(lanes + kColP + 16 * m, p);
                     }
-                    tmem_st16(lanes + kColP + 16 * m, p);
-                }
-                tmem_wait_st();
-                fence_before_sync();
-                mbar_arrive_local(p_ready);
+                    tmem_wait_st();
+                    fence_before_sync();
+                    mbar_arrive_local(p_ready);
 
-                float o[DV];
-                wait(inter_done, i);
-                fence_after_sync();
+                    float o[DV];
+                    wait(inter_done, i);
+                    fence_after_sync();
 #pragma unroll
-                for (int x = 0; x < DV; x += 32) tmem_ld32(lanes + kColO + x, o + x);
-                tmem_wait_ld();
-                fence_before_sync();
-                mbar_arrive_local(inter_read);
-                const int e = rev ? n - 1 - r : r + 1;
-                const float2 f = splat2(out_scale * tab[max(e, 0)]);   // rows past the sequence are not stored
-                wait(intra_done, i);
-                fence_after_sync();
-                unsigned char* so = smem + (size_t)st * C::kStage;   // over the block's tiles, which are done with
-                float y2[2][16];
-                tmem_ld16(lanes + kColO, y2[0]);
-#pragma unroll
-                for (int x = 0; x < DV; x += 16) {
-                    float* v = y2[(x >> 4) & 1];
+                    for (int x = 0; x < DV; x += 32) tmem_ld32(lanes + kColO + x, o + x);
                     tmem_wait_ld();
-                    if (x + 16 < DV) tmem_ld16(lanes + kColO + x + 16, y2[((x >> 4) + 1) & 1]);
+                    fence_before_sync();
+                    mbar_arrive_local(inter_read);
+                    const int e = rev ? n - 1 - r : r + 1;
+                    const float2 f = splat2(out_scale * tab[max(e, 0)]);     // rows past the sequence are not stored
+                    wait(intra_done, i);
+                    fence_after_sync();
+                    unsigned char* so = smem + (size_t)st * C::kStage;       // over the block's tiles, which are done with
+                    float y2[2][16];
+                    tmem_ld16(lanes + kColO, y2[0]);
 #pragma unroll
-                    for (int y = 0; y < 16; y += 2) {
-                        const float2 t = fma2(f, make_float2(o[x + y], o[x + y + 1]), make_float2(v[y], v[y + 1]));
-                        v[y] = t.x;
-                        v[y + 1] = t.y;
+                    for (int x = 0; x < DV; x += 16) {
+                        float* v = y2[(x >> 4) & 1];
+                        tmem_wait_ld();
+                        if (x + 16 < DV) tmem_ld16(lanes + kColO + x + 16, y2[((x >> 4) + 1) & 1]);
+#pragma unroll
+                        for (int y = 0; y < 16; y += 2) {
+                            const float2 t = fma2(f, make_float2(o[x + y], o[x + y + 1]), make_float2(v[y], v[y + 1]));
+                            v[y] = t.x;
+                            v[y + 1] = t.y;
+                        }
+                        if (o_f32) {                               // tiles of 32 columns
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                *reinterpret_cast<float4*>(so + (x / 32) * kAtom + r * 128 + (((y + (x & 16) / 4) ^ (r & 7)) << 4)) =
+                                    make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+                        } else {                                   // tiles of 64
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                *reinterpret_cast<uint4*>(so + (x / 64) * kAtom + r * 128 + (((y + (x & 48) / 8) ^ (r & 7)) << 4)) =
+                                    make_uint4(pack_bf16x2(v[8 * y], v[8 * y + 1]), pack_bf16x2(v[8 * y + 2], v[8 * y + 3]),
+                                               pack_bf16x2(v[8 * y + 4], v[8 * y + 5]), pack_bf16x2(v[8 * y + 6], v[8 * y + 7]));
+                        }
                     }
-                    if (o_f32) {                                     // tiles of 32 columns
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            *reinterpret_cast<float4*>(so + (x / 32) * kAtom + r * 128 + (((y + (x & 16) / 4) ^ (r & 7)) << 4)) =
-                                make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
-                    } else {                                         // tiles of 64
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            *reinterpret_cast<uint4*>(so + (x / 64) * kAtom + r * 128 + (((y + (x & 48) / 8) ^ (r & 7)) << 4)) =
-                                make_uint4(pack_bf16x2(v[8 * y], v[8 * y + 1]), pack_bf16x2(v[8 * y + 2], v[8 * y + 3]),
-                                           pack_bf16x2(v[8 * y + 4], v[8 * y + 5]), pack_bf16x2(v[8 * y + 6], v[8 * y + 7]));
+                    fence_before_sync();
+                    mbar_arrive_local(o_free);
+                    if (n < kB) {   // rows behind the sequence may be another's: plain stores of its own rows
+                        named_sync(1, 128);
+                        const int64_t row = wk->row0 + (int64_t)b * kB;
+                        const int es = o_f32 ? 4 : 2, chunks = DV * es / 16;
+                        unsigned char* dst = (unsigned char*)s.o;
+                        for (int id = tid; id < n * chunks; id += 128) {
+                            const int rr = id / chunks, ch = id % chunks;
+                            *reinterpret_cast<uint4*>(dst + ((row + rr) * s.o_ld + (int64_t)wk->head * DV) * es + ch * 16) =
+                                *reinterpret_cast<const uint4*>(so + (ch >> 3) * kAtom + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                        }
                     }
+                    fence_async_smem();
+                    mbar_arrive_local(o_staged);
                 }
-                fence_before_sync();
-                mbar_arrive_local(o_free);
-                if (n < kB) {   // rows behind the sequence may be another's: plain stores of its own rows
-                    named_sync(1, 128);
-                    const int64_t row = it.row0 + (int64_t)b * kB;
-                    const int es = s.o_f32 ? 4 : 2, chunks = DV * es / 16;
-                    unsigned char* dst = (unsigned char*)s.o;
-                    for (int id = tid; id < n * chunks; id += 128) {
-                        const int rr = id / chunks, ch = id % chunks;
-                        *reinterpret_cast<uint4*>(dst + ((row + rr) * s.o_ld + (int64_t)h * DV) * es + ch * 16) =
-                            *reinterpret_cast<const uint4*>(so + (ch >> 3) * kAtom + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
-                    }
-                }
-                fence_async_smem();
-                mbar_arrive_local(o_staged);
+                close(k);
             }
         }
     } else if (warp < 8) {
         // ------------------------------------------------------------------ the state
-        regs_up<kRegsState>();
+        regs_up<STATES ? kRegsStateOnly : kRegsState>();
         const int d = tid - 128;                                   // state row = TMEM lane
         const uint32_t lanes = tmem + ((uint32_t)((warp - 4) * 32) << 16);
         const bool mine = d < DV;
         const int64_t hs = (int64_t)DK * DV;
-        float S[DK];
+        unsigned char* buf = smem + C::kOffS + (size_t)(warp - 4) * 32 * (DK * 2);   // this warp's rows of the operand copy's room
+        int i = 0;
+        for (int k = 0;; ++k) {
+            const Work* wk = open(k, 4, 128);
+            if (!wk) break;
+            const LinearScan& s = a.s[wk->scan];
+            const int flags = wk->flags, nall = wk->n, nb = (nall + kB - 1) / kB;
+            const bool rev = s.reverse;
+            // the operand copy of the segment before has been read
+            if (!STATES && i > 0) wait(inter_done, i - 1);
+            float S[DK];
 #pragma unroll
-        for (int e = 0; e < DK; ++e) S[e] = 0.0f;
-        if (!STATES && mine) {
-            if (it.nseg > 1) {       // never the slot itself: the row's last segment may be rewriting it
-                const float4* p = reinterpret_cast<const float4*>(s.seg_states + (item * c.H + h) * hs + (int64_t)d * DK);
+            for (int e = 0; e < DK; ++e) S[e] = 0.0f;
+            if (!STATES && mine) {
+                if (flags & kSplit) {    // never the slot itself: the row's last segment may be rewriting it
+                    load_state<DK>(s.seg_states + ((int64_t)wk->item * c.H + wk->head) * hs + (int64_t)(d - lane) * DK, buf, lane, S);
+                } else if (flags & kFirstInit) {
+                    const float* p = s.init + ((int64_t)wk->slot * c.H + wk->head) * hs;
+                    if (s.init_cs == 1) {
+                        load_state<DK>(p + (int64_t)(d - lane) * DK, buf, lane, S);
+                    } else {
+                        p += (int64_t)d * s.init_rs;
 #pragma unroll
-                for (int e = 0; e < DK / 4; ++e) {
-                    const float4 x = p[e];
-                    S[4 * e] = x.x; S[4 * e + 1] = x.y; S[4 * e + 2] = x.z; S[4 * e + 3] = x.w;
-                }
-            } else if (linear_has_init(c, s, it.seq)) {
-                const float* p = s.init + (it.slot * c.H + h) * hs + (int64_t)d * s.init_rs;
-                if (s.init_cs == 1) {
+                        for (int e = 0; e < DK; e += 8) {   // 8 addresses at a time: more would not fit in registers
 #pragma unroll
-                    for (int e = 0; e < DK / 4; ++e) {
-                        const float4 x = reinterpret_cast<const float4*>(p)[e];
-                        S[4 * e] = x.x; S[4 * e + 1] = x.y; S[4 * e + 2] = x.z; S[4 * e + 3] = x.w;
+                            for (int x = 0; x < 8; ++x) S[e + x] = p[x * s.init_cs];
+                            p += 8 * s.init_cs;
+                            asm volatile("" : "+l"(p)::"memory");
+                        }
                     }
-                } else {
+                }
+            }
+            // a warp's room for whole states holds other warps' rows of the operand copy
+            if (!STATES) named_sync(4, 128);
+            const float g = wk->log_l;
+            for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                if constexpr (!STATES) {     // S in bf16, the K-major operand of inter
+                    if (x0 > 0) wait(inter_done, i - 1);
+                    if (mine) {
 #pragma unroll
-                    for (int e = 0; e < DK; e += 8) {       // 8 addresses at a time: more would not fit in registers
+                        for (int e = 0; e < DK; e += 8)
+                            *reinterpret_cast<uint4*>(smem + C::kOffS + (e / 64) * (DV * 128) + d * 128 + ((((e & 63) >> 3) ^ (d & 7)) << 4)) =
+                                make_uint4(pack_bf16x2(S[e], S[e + 1]), pack_bf16x2(S[e + 2], S[e + 3]),
+                                           pack_bf16x2(S[e + 4], S[e + 5]), pack_bf16x2(S[e + 6], S[e + 7]));
+                    }
+                    fence_async_smem();
+                    mbar_arrive_local(s_ready);
+                }
+                const LinearDecay dec(g * (float)tokens(nall, block(rev, nb, x0)));
+                const float2 f2 = splat2(dec.f), keep2 = splat2(dec.slow ? 1.0f : 0.0f);
+                wait(u_done, i);
+                fence_after_sync();
+                float u2[2][16];
+                tmem_ld16(lanes + kColU, u2[0]);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) S[e + x] = p[x * s.init_cs];
-                        p += 8 * s.init_cs;
-                        asm volatile("" : "+l"(p)::"memory");
+                for (int e = 0; e < DK; e += 16) {
+                    float* u = u2[(e >> 4) & 1];
+                    tmem_wait_ld();
+                    if (e + 16 < DK) tmem_ld16(lanes + kColU + e + 16, u2[((e >> 4) + 1) & 1]);
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {          // LinearDecay::step, both kinds in one code
+                        const float2 S2 = make_float2(S[e + x], S[e + x + 1]);
+                        const float2 t = fma2(f2, S2, fma2(keep2, S2, make_float2(u[x], u[x + 1])));
+                        S[e + x] = t.x;
+                        S[e + x + 1] = t.y;
                     }
                 }
+                fence_before_sync();
+                mbar_arrive_local(u_free);
             }
-        }
-        auto publish = [&]() {       // S in bf16, the K-major operand of inter
-            if constexpr (!STATES) {
-                if (mine) {
-#pragma unroll
-                    for (int e = 0; e < DK; e += 8)
-                        *reinterpret_cast<uint4*>(smem + C::kOffS + (e / 64) * (DV * 128) + d * 128 + ((((e & 63) >> 3) ^ (d & 7)) << 4)) =
-                            make_uint4(pack_bf16x2(S[e], S[e + 1]), pack_bf16x2(S[e + 2], S[e + 3]),
-                                       pack_bf16x2(S[e + 4], S[e + 5]), pack_bf16x2(S[e + 6], S[e + 7]));
-                }
-                fence_async_smem();
-                mbar_arrive_local(s_ready);
+            float* out = nullptr;
+            if (STATES) out = s.seg_states + ((int64_t)wk->item * c.H + wk->head) * hs;
+            else if ((flags & kFinal) && s.final_state) out = s.final_state + ((int64_t)wk->slot * c.H + wk->head) * hs;
+            if (out) {
+                if (!STATES && nb > 0) wait(inter_done, i - 1);
+                if (mine) store_state<DK>(out + (int64_t)(d - lane) * DK, buf, lane, S);
             }
-        };
-        if (nb > 0) publish();
-        const LinearDecay whole((float)(g * kB));
-        for (int i = 0; i < nb; ++i) {
-            const int n = tokens(block(i));
-            const LinearDecay dec = n == kB ? whole : LinearDecay((float)(g * n));
-            const float2 f2 = splat2(dec.f), keep2 = splat2(dec.slow ? 1.0f : 0.0f);
-            wait(u_done, i);
-            fence_after_sync();
-            float u2[2][16];
-            tmem_ld16(lanes + kColU, u2[0]);
-#pragma unroll
-            for (int e = 0; e < DK; e += 16) {
-                float* u = u2[(e >> 4) & 1];
-                tmem_wait_ld();
-                if (e + 16 < DK) tmem_ld16(lanes + kColU + e + 16, u2[((e >> 4) + 1) & 1]);
-#pragma unroll
-                for (int x = 0; x < 16; x += 2) {          // LinearDecay::step, both kinds in one code
-                    const float2 S2 = make_float2(S[e + x], S[e + x + 1]);
-                    const float2 t = fma2(f2, S2, fma2(keep2, S2, make_float2(u[x], u[x + 1])));
-                    S[e + x] = t.x;
-                    S[e + x + 1] = t.y;
-                }
-            }
-            fence_before_sync();
-            mbar_arrive_local(u_free);
-            if (i + 1 < nb) {
-                if (!STATES) wait(inter_done, i);        // the operand copy of S has been read
-                publish();
-            }
-        }
-        float* out = nullptr;
-        if (STATES) out = s.seg_states + (item * c.H + h) * hs;
-        else if (last && s.final_state) out = s.final_state + (it.slot * c.H + h) * hs;
-        if (out && mine) {
-            float4* p = reinterpret_cast<float4*>(out + (int64_t)d * DK);
-#pragma unroll
-            for (int e = 0; e < DK / 4; ++e) p[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+            close(k);
         }
     } else {
-        // ------------------------------------------------------------------ one thread each
+        // ------------------------------------------------------------------ one warp each
         regs_down<kRegsCtl>();
-        if (warp == 12 && lane == 0) {                             // loads
-            const ScanMaps& m = maps.m[z];
-            for (int i = 0; i < nb; ++i) {
-                const int st = i % C::kStages;
-                const uint32_t dst = sb + (uint32_t)st * C::kStage;
-                const int row = (int)(it.row0 + (int64_t)block(i) * kB);
-                if (i >= C::kStages) wait(kv_empty(st), i / C::kStages - 1);
-                mbar_arrive_expect_tx(kv_full(st), C::kK + C::kV);
-                for (int x = 0; x < DV / 64; ++x)
-                    tma_load_3d(dst + C::kQ + C::kK + x * kAtom, &m.v, (h / s.v_share) * DV + 64 * x, row, 0, kv_full(st));
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_3d(dst + C::kQ + x * kAtom, &m.k, (h / s.k_share) * DK + 64 * x, row, 0, kv_full(st));
-                if constexpr (!STATES) {
-                    if (i >= C::kStages) wait(q_empty(st), i / C::kStages - 1);
-                    mbar_arrive_expect_tx(q_full(st), C::kQ);
-                    for (int x = 0; x < DK / 64; ++x)
-                        tma_load_3d(dst + x * kAtom, &m.q, (h / s.q_share) * DK + 64 * x, row, 0, q_full(st));
+        if (warp == 12) {                                          // loads
+            int i = 0;
+            for (int k = 0;; ++k) {
+                const Work* wk = open(k, 0, 32);
+                if (!wk) break;
+                if (lane == 0) {
+                    const LinearScan& s = a.s[wk->scan];
+                    const ScanMaps& m = maps.m[wk->scan];
+                    const int nb = (wk->n + kB - 1) / kB, h = wk->head;
+                    const int cq = h / s.q_share * DK, ck = h / s.k_share * DK, cv = h / s.v_share * DV;
+                    for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                        const int st = i % C::kStages;
+                        const uint32_t dst = sb + (uint32_t)st * C::kStage;
+                        const int row = wk->row0 + block(s.reverse, nb, x0) * kB;
+                        if (i >= C::kStages) wait(kv_empty(st), i / C::kStages - 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(kv_full(st), C::kK + C::kV);
+                        for (int x = 0; x < DV / 64; ++x)
+                            tma_load_3d(dst + C::kQ + C::kK + x * kAtom, &m.v, cv + 64 * x, row, 0, kv_full(st));
+                        for (int x = 0; x < DK / 64; ++x)
+                            tma_load_3d(dst + C::kQ + x * kAtom, &m.k, ck + 64 * x, row, 0, kv_full(st));
+                        if constexpr (!STATES) {
+                            if (i >= C::kStages) wait(q_empty(st), i / C::kStages - 1);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(q_full(st), C::kQ);
+                            for (int x = 0; x < DK / 64; ++x)
+                                tma_load_3d(dst + x * kAtom, &m.q, cq + 64 * x, row, 0, q_full(st));
+                        }
+                    }
                 }
+                close(k);
             }
+            // nothing is in flight when the block ends, whatever gave up
+            if (lane == 0)
+                for (int x = max(0, i - C::kStages); x < i; ++x) {
+                    mbar_wait_bounded(kv_full(x % C::kStages), (uint32_t)(x / C::kStages & 1), kWait);
+                    if (!STATES) mbar_wait_bounded(q_full(x % C::kStages), (uint32_t)(x / C::kStages & 1), kWait);
+                }
         } else if (warp == 13) {                                   // MMAs: the warp waits, one lane issues
             const bool leader = elect_one();
-            for (int i = 0; i < nb; ++i) {
-                const int st = i % C::kStages;
-                const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK, ss = sb + C::kOffS;
-                // descriptors count addresses in 16 bytes
-                const uint64_t kmn = sdesc_sw128_mn(sk);
-                wait(kv_full(st), i / C::kStages);
-                if (!STATES) wait(q_full(st), i / C::kStages);
-                fence_after_sync();
-                if constexpr (!STATES) {
-                    const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), sd = sdesc_sw128(ss);
-                    if (leader) {
-#pragma unroll
-                        for (int x = 0; x < DK / 16; ++x) {
-                            const uint64_t at = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
-                            mma_bf16(tmem + kColP, qd + at, kd + at, idesc_bf16(128, 128, 0, 0), x > 0);
-                        }
-                        mma_commit(qk_done);
-                    }
-                    __syncwarp();
-                    wait(s_ready, i);
-                    if (i > 0) wait(o_free, i - 1);
+            int i = 0;
+            for (int k = 0;; ++k) {
+                const Work* wk = open(k, 0, 32);
+                if (!wk) break;
+                // o is staged over Q's tiles; k's and v's are free as soon as the block's MMAs are done,
+                // unless o is larger than q
+                const bool kv_early = STATES || (DV <= DK && !a.s[wk->scan].o_f32);
+                const int nb = (wk->n + kB - 1) / kB;
+                close(k);
+                for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                    const int st = i % C::kStages;
+                    const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK, ss = sb + C::kOffS;
+                    // descriptors count addresses in 16 bytes
+                    const uint64_t kmn = sdesc_sw128_mn(sk);
+                    wait(kv_full(st), i / C::kStages);
+                    if (!STATES) wait(q_full(st), i / C::kStages);
                     fence_after_sync();
-                    if (leader) {
+                    if constexpr (!STATES) {
+                        const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), sd = sdesc_sw128(ss);
+                        if (leader) {
 #pragma unroll
-                        for (int x = 0; x < DK / 16; ++x)
-                            mma_bf16(tmem + kColO, qd + (((x >> 2) * kAtom + (x & 3) * 32) >> 4),
-                                     sd + (((x >> 2) * (DV * 128) + (x & 3) * 32) >> 4), idesc_bf16(128, DV, 0, 0), x > 0);
-                        mma_commit(inter_done);
+                            for (int x = 0; x < DK / 16; ++x) {
+                                const uint64_t at = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
+                                mma_bf16(tmem + kColP, qd + at, kd + at, idesc_bf16(128, 128, 0, 0), x > 0);
+                            }
+                            mma_commit(qk_done);
+                        }
+                        __syncwarp();
+                        wait(s_ready, i);
+                        if (i > 0) wait(o_free, i - 1);
+                        fence_after_sync();
+                        if (leader) {
+#pragma unroll
+                            for (int x = 0; x < DK / 16; ++x)
+                                mma_bf16(tmem + kColO, qd + (((x >> 2) * kAtom + (x & 3) * 32) >> 4),
+                                         sd + (((x >> 2) * (DV * 128) + (x & 3) * 32) >> 4), idesc_bf16(128, DV, 0, 0), x > 0);
+                            mma_commit(inter_done);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                if (i > 0) wait(u_free, i - 1);
+                    if (i > 0) wait(u_free, i - 1);
 #pragma unroll 1
-                for (int u = 0; u < kB / kSub; ++u) {
-                    const int k = i * (kB / kSub) + u;
-                    wait(v_ready(k & 1), k >> 1);
-                    fence_after_sync();
-                    const uint32_t at = tmem + kColV + (uint32_t)(k & 1) * kSlotCols;
-                    if (leader) {
+                    for (int u = 0; u < kB / kSub; ++u) {
+                        const int kk = i * (kB / kSub) + u;
+                        wait(v_ready(kk & 1), kk >> 1);
+                        fence_after_sync();
+                        const uint32_t at = tmem + kColV + (uint32_t)(kk & 1) * kSlotCols;
+                        if (leader) {
 #pragma unroll
-                        for (int x = 0; x < kSub / 16; ++x)
+                            for (int x = 0; x < kSub / 16; ++x)
 #pragma unroll
-                            for (int t = 0; t < 3; ++t)
-                                mma_bf16_ts(tmem + kColU, at + t * 16 + x * 8, kmn + (uint64_t)((u * kSub + x * 16) * 128 >> 4),
-                                            idesc_bf16(128, DK, 0, 1), u + x + t > 0);
-                        mma_commit(v_free(k & 1));
-                        if (u == kB / kSub - 1) {
-                            mma_commit(u_done);
-                            if (STATES) mma_commit(kv_empty(st));
+                                for (int t = 0; t < 3; ++t)
+                                    mma_bf16_ts(tmem + kColU, at + t * 16 + x * 8, kmn + (uint64_t)((u * kSub + x * 16) * 128 >> 4),
+                                                idesc_bf16(128, DK, 0, 1), u + x + t > 0);
+                            mma_commit(v_free(kk & 1));
+                            if (u == kB / kSub - 1) {
+                                mma_commit(u_done);
+                                if (STATES) mma_commit(kv_empty(st));
+                            }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                if constexpr (!STATES) {
-                    wait(p_ready, i);
-                    wait(inter_read, i);
-                    fence_after_sync();
-                    const uint64_t vmn = sdesc_sw128_mn(sv);
-                    if (leader) {
+                    if constexpr (!STATES) {
+                        wait(p_ready, i);
+                        wait(inter_read, i);
+                        fence_after_sync();
+                        const uint64_t vmn = sdesc_sw128_mn(sv);
+                        if (leader) {
 #pragma unroll
-                        for (int x = 0; x < kB / 16; ++x)
-                            mma_bf16_ts(tmem + kColO, tmem + kColP + x * 8, vmn + (uint64_t)(x * 2048 >> 4), idesc_bf16(128, DV, 0, 1), x > 0);
-                        mma_commit(intra_done);
-                        if (kv_early) mma_commit(kv_empty(st));
+                            for (int x = 0; x < kB / 16; ++x)
+                                mma_bf16_ts(tmem + kColO, tmem + kColP + x * 8, vmn + (uint64_t)(x * 2048 >> 4), idesc_bf16(128, DV, 0, 1), x > 0);
+                            mma_commit(intra_done);
+                            if (kv_early) mma_commit(kv_empty(st));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
-        } else if (warp == 14 && lane == 0 && !STATES) {           // stores
-            const int per = s.o_f32 ? 32 : 64;
-            for (int i = 0; i < nb; ++i) {
-                const int st = i % C::kStages, b = block(i);
-                wait(o_staged, i);
-                if (tokens(b) == kB) {
-                    for (int x = 0; x < DV / per; ++x)
-                        tma_store_3d(&maps.m[z].o, sb + (uint32_t)st * C::kStage + x * kAtom, h * DV + per * x,
-                                     (int)(it.row0 + (int64_t)b * kB), 0);
-                    bulk_commit();
-                    bulk_wait_read_all();
-                }
-                mbar_arrive_local(q_empty(st));
-                if (!kv_early) mbar_arrive_local(kv_empty(st));
+            if (i > 0) {
+                mbar_wait_bounded(u_done, (uint32_t)((i - 1) & 1), kWait);
+                if (!STATES) mbar_wait_bounded(intra_done, (uint32_t)((i - 1) & 1), kWait);
             }
-            bulk_wait_all();
+        } else if (warp == 14 && !STATES) {                        // stores
+            int i = 0;
+            for (int k = 0;; ++k) {
+                const Work* wk = open(k, 0, 32);
+                if (!wk) break;
+                if (lane == 0) {
+                    const LinearScan& s = a.s[wk->scan];
+                    const CUtensorMap* m = &maps.m[wk->scan].o;
+                    const bool kv_early = DV <= DK && !s.o_f32;
+                    const int per = s.o_f32 ? 32 : 64, nb = (wk->n + kB - 1) / kB, c0 = wk->head * DV;
+                    for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                        const int st = i % C::kStages, b = block(s.reverse, nb, x0);
+                        wait(o_staged, i);
+                        if (tokens(wk->n, b) == kB) {
+                            for (int x = 0; x < DV / per; ++x)
+                                tma_store_3d(m, sb + (uint32_t)st * C::kStage + x * kAtom, c0 + per * x, wk->row0 + b * kB, 0);
+                            bulk_commit();
+                            bulk_wait_read_all();
+                        }
+                        mbar_arrive_local(q_empty(st));
+                        if (!kv_early) mbar_arrive_local(kv_empty(st));
+                    }
+                }
+                close(k);
+            }
+            if (lane == 0) bulk_wait_all();
+        } else if (warp == 15) {                                   // the list of segments
+            const int64_t total = c.items * c.H * a.nscans;
+            int k = 0;
+            for (int64_t w = blockIdx.x;; w += gridDim.x) {
+                const bool end = w >= total;
+                LinearItem it{};
+                const int z = (int)(w % a.nscans);
+                const int64_t ih = w / a.nscans;
+                const int h = (int)(ih % c.H);
+                const bool rev = a.s[z].reverse;
+                if (!end) {
+                    if (!linear_item(c, ih / c.H, &it)) continue;
+                    if (STATES && (rev ? it.seg == 0 : it.seg == it.nseg - 1)) continue;   // nothing follows it
+                }
+                if (k >= 2) wait(w_empty(k & 1), (k >> 1) - 1);
+                Work* wk = works + (k & 1);
+                if (!end) {
+                    // l^e in fp32: g e as the sum of a product and its rounding error
+                    const float g = linear_log_decay(c.log_decay, h);
+                    auto power = [&](int e) {
+                        const float p = g * (float)e;
+                        return expf(p) * (1.0f + fmaf(g, (float)e, -p));
+                    };
+#pragma unroll 1
+                    for (int e = lane; e <= kB; e += 32) wk->tab[e] = power(e);
+                    wk->wtab[lane] = power(rev ? lane : 31 - lane);
+                    if (lane == 0) {
+                        wk->log_l = g;
+                        wk->row0 = (int)it.row0;
+                        wk->scan = z;
+                        wk->head = h;
+                        wk->slot = (int)it.slot;
+                        wk->item = (int)(ih / c.H);
+                        wk->flags = (linear_has_init(c, a.s[z], it.seq) ? kFirstInit : 0) | (it.nseg > 1 ? kSplit : 0) |
+                                    ((rev ? it.seg == 0 : it.seg == it.nseg - 1) ? kFinal : 0);
+                    }
+                }
+                if (lane == 0) wk->n = end ? -1 : (int)it.n;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(w_full(k & 1));
+                ++k;
+                if (end || !ok) break;
+            }
         }
     }
     if (!ok) set_device_status(c.status, kDevTimeout);
@@ -646,7 +817,8 @@ cudaError_t launch_one(const TcArgs& a, const TcMaps& m, cudaStream_t st)
     cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<DK, DV, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     LaunchScope ls(STATES ? "linear_tc_states" : "linear_tc", st);
-    linear_tc_kernel<DK, DV, STATES><<<(unsigned)(a.c.items * a.c.H * a.nscans), kThreads, C::kSmem, st>>>(a, m);
+    const int64_t total = a.c.items * a.c.H * a.nscans, sms = device_sm_count();
+    linear_tc_kernel<DK, DV, STATES><<<(unsigned)(total < sms ? total : sms), kThreads, C::kSmem, st>>>(a, m);
     return cudaGetLastError();
 }
 
