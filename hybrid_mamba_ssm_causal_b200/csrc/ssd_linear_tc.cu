@@ -17,18 +17,18 @@
 //
 // One CTA per SM, which takes segment after segment; a row that is cut into several has their own
 // states computed first (the same kernel without q and o) and joined by a small kernel between.
-// Four warpgroups, so that the next block's (and the next segment's) loads, w V and scores are under
-// way while this one's state and outputs are finished; registers are moved to the two that hold tiles
-// (setmaxnreg):
-//   0  outputs, a row i each: scores -> P, then o = c l^{i+1} inter + intra, staged over the block's
-//      own tiles for a TMA store
-//   1  state, a row d each: S += U, and its operand copy
-//   2  w V: V's tile transposed by ldmatrix, times w, into TMEM, 32 tokens at a time in two slots
-//   3  one warp each for TMA loads, every MMA, the stores, and the list of segments: where each lies
-//      and its head's powers of l, one segment ahead
-// TMEM columns: QK and, over its first half, P; one output tile (inter is read out before intra
-// overwrites it); U; the two slots of w V. The loops are kept rolled where registers allow: the four
-// warpgroups' code competes for the instruction cache. Nothing may spill: beside 227 KB of shared
+// Five warpgroups, so that the next block's (and the next segment's) loads, w V and scores are under
+// way while this one's state and outputs are finished; registers are moved to the one that holds a
+// tile in them (setmaxnreg):
+//   0    outputs, a row i each: scores -> P; inter times c l^{i+1}, in place, for intra to add to; then
+//        o, staged over the block's own tiles for a TMA store
+//   1    state, a row d each: S += U, and its operand copy
+//   2, 3 w V: V's tile transposed by ldmatrix, times w, into TMEM, 32 tokens at a time in a slot each
+//   4    a warp for the list of segments (where each lies and its head's powers of l, one segment ahead)
+//        and their TMA loads, one for the stores, one for the MMAs of the outputs and one for those of the
+//        state, which would otherwise wait for one another
+// TMEM columns: QK and, over its first half, P; one output tile; U; the two slots of w V. The loops are
+// kept rolled where registers allow: the warpgroups' code competes for the instruction cache. Nothing may spill: beside 227 KB of shared
 // memory the L1 has some 16 KB left.
 //
 // No decay factor is ever above 1: off the diagonal 32 x 32 tiles, l^{i-j} = l^{i-j0-31} l^{31-(j-j0)}.
@@ -49,18 +49,17 @@ namespace {
 using namespace tc;
 
 constexpr int kB = 128;                  // tokens per block
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr uint32_t kAtom = 128 * 128;    // one [128 rows][128 bytes] swizzled tile
 constexpr uint32_t kSmemMax = 232448;
 constexpr long long kWait = 4000000000LL;   // ~2 s at 2 GHz
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColV = 384;
 constexpr int kSub = 32;                 // tokens of one slot of w V
 constexpr uint32_t kSlotCols = 64;       // its TMEM columns: three terms of 16, and 16 unused
-// Registers per thread of the four warpgroups; they share what the launch gave them (512 x 128).
-constexpr int kRegsOut = 208, kRegsState = 184, kRegsV = 72, kRegsCtl = 48;
-constexpr int kRegsStateOnly = 208;      // where warpgroup 0 makes w V too
-static_assert(kRegsOut + kRegsState + kRegsV + kRegsCtl <= 4 * 128, "more registers than the launch's");
-static_assert(2 * kRegsV + kRegsStateOnly + kRegsCtl <= 4 * 128, "more registers than the launch's");
+// Registers per thread of the warpgroups (outputs; state; the two of w V; the last); they share what
+// the launch gave them (640 x 96).
+constexpr int kRegsOut = 88, kRegsState = 200, kRegsV = 72, kRegsCtl = 48;
+static_assert(kRegsOut + kRegsState + 2 * kRegsV + kRegsCtl <= 5 * 96, "more registers than the launch's");
 
 template <int DK, int DV, bool STATES>
 struct Cfg {
@@ -96,6 +95,9 @@ struct TcArgs {
     LinearCall c;
     LinearScan s[kMaxScans];
     int nscans;
+    // o of every scan fits over q's tiles, so that k's and v's are free as soon as the block's MMAs are
+    // done; otherwise o takes k's and v's place too, and the state's MMAs stay a block behind the outputs
+    bool early;
 };
 struct TcMaps {
     ScanMaps m[kMaxScans];
@@ -223,14 +225,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                    u_free = bar0 + 256, s_ready = bar0 + 264;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 272);
     static_assert(C::kOffBar + 276 <= C::kSmem, "barriers");
-    constexpr int kReaders = STATES ? 14 : 15;   // warps that read a work slot
+    constexpr int kReaders = STATES ? 13 : 19;   // warps that read a work slot
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
             mbar_init(kv_full(i), 1);
-            mbar_init(kv_empty(i), 1);
+            mbar_init(kv_empty(i), STATES ? 1 : 2);   // U's MMAs, and intra's or the stores
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(v_ready(i), 128);
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         mbar_init(s_ready, 128);
         fence_mbar_init();
     }
-    if (warp == 13) tmem_alloc(smem_u32(tmem_slot), 512);
+    if (warp == 17) tmem_alloc(smem_u32(tmem_slot), 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -275,11 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     auto block = [&](bool rev, int nb, int x) { return rev ? nb - 1 - x : x; };
     auto tokens = [&](int n, int b) { return min(n - b * kB, kB); };
 
-    if (STATES ? warp < 4 || (warp >= 8 && warp < 12) : warp >= 8 && warp < 12) {
+    if (warp >= 8 && warp < 16) {
         // ------------------------------------------------------------------ w V
-        // where no outputs are wanted, warpgroup 0 takes every other sub-block (and slot)
+        // two warpgroups, every other sub-block (and slot) each
         regs_down<kRegsV>();
-        const int first = STATES && warp < 4 ? 1 : 0, step = STATES ? 2 : 1;
+        const int first = warp < 12 ? 0 : 1;
         const int q = warp & 3;                                    // TMEM lanes, and rows d, 32 q ..
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + kColV;
         const bool mine = 32 * q < DV;
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         }
         int i = 0;                                                 // blocks so far
         for (int k = 0;; ++k) {
-            const Work* wk = open(k, STATES ? 3 : 2, STATES ? 256 : 128);
+            const Work* wk = open(k, 3, 256);
             if (!wk) break;
             const bool rev = a.s[wk->scan].reverse;
             const float us = a.s[wk->scan].u_scale;
@@ -314,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     named_sync(2, 128);
                     fence_async_smem();
                 }
-                if (n < kB && step == 2) named_sync(3, 256);
+                if (n < kB) named_sync(3, 256);
 #pragma unroll 1
-                for (int u = first; u < kB / kSub; u += step) {
+                for (int u = first; u < kB / kSub; u += 2) {
                     const int kk = i * (kB / kSub) + u;
                     if (kk >= 2) wait(v_free(kk & 1), (kk >> 1) - 1);
                     fence_after_sync();
@@ -368,9 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             }
             close(k);
         }
-    } else if (!STATES && warp < 4) {
+    } else if (warp < 4) {
         // ------------------------------------------------------------------ scores and outputs
-        regs_up<kRegsOut>();
+        regs_down<kRegsOut>();
         if constexpr (!STATES) {
             const int r = tid;                                     // row i of the block = TMEM lane
             const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
@@ -427,45 +429,55 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         }
                         tmem_st16(lanes + kColP + 16 * m, p);
                     }
+                    if (n < kB) {     // P's zeros must not meet what rows behind the sequence hold
+                        unsigned char* sv = smem + (size_t)st * C::kStage + C::kQ + C::kK + (n + r) * 128;
+                        if (n + r < kB)
+                            for (int x = 0; x < 8 * (DV / 64); ++x) *reinterpret_cast<uint4*>(sv + (x >> 3) * kAtom + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                    }
                     tmem_wait_st();
                     fence_before_sync();
                     mbar_arrive_local(p_ready);
 
-                    float o[DV];
-                    wait(inter_done, i);
-                    fence_after_sync();
-#pragma unroll
-                    for (int x = 0; x < DV; x += 32) tmem_ld32(lanes + kColO + x, o + x);
-                    tmem_wait_ld();
-                    fence_before_sync();
-                    mbar_arrive_local(inter_read);
+                    // inter's row times c l^{i+1}, back as what intra adds to
                     const int e = rev ? n - 1 - r : r + 1;
                     const float2 f = splat2(out_scale * tab[max(e, 0)]);     // rows past the sequence are not stored
-                    wait(intra_done, i);
+                    wait(inter_done, i);
                     fence_after_sync();
-                    unsigned char* so = smem + (size_t)st * C::kStage;       // over the block's tiles, which are done with
-                    float y2[2][16];
-                    tmem_ld16(lanes + kColO, y2[0]);
-#pragma unroll
-                    for (int x = 0; x < DV; x += 16) {
-                        float* v = y2[(x >> 4) & 1];
+#pragma unroll 1
+                    for (int x = 0; x < DV; x += 32) {
+                        float v[32];
+                        tmem_ld32(lanes + kColO + x, v);
                         tmem_wait_ld();
-                        if (x + 16 < DV) tmem_ld16(lanes + kColO + x + 16, y2[((x >> 4) + 1) & 1]);
 #pragma unroll
-                        for (int y = 0; y < 16; y += 2) {
-                            const float2 t = fma2(f, make_float2(o[x + y], o[x + y + 1]), make_float2(v[y], v[y + 1]));
+                        for (int y = 0; y < 32; y += 2) {
+                            const float2 t = mul2(f, make_float2(v[y], v[y + 1]));
                             v[y] = t.x;
                             v[y + 1] = t.y;
                         }
+                        tmem_st32(lanes + kColO + x, v);
+                    }
+                    tmem_wait_st();
+                    fence_before_sync();
+                    mbar_arrive_local(inter_read);
+                    wait(intra_done, i);
+                    if (!a.early) wait(u_done, i);               // k and v too have been read
+                    fence_after_sync();
+                    unsigned char* so = smem + (size_t)st * C::kStage + r * 128;   // over the block's tiles, which are done with
+#pragma unroll 1
+                    for (int x = 0; x < DV; x += 32) {
+                        float v[32];
+                        tmem_ld32(lanes + kColO + x, v);
+                        tmem_wait_ld();
                         if (o_f32) {                               // tiles of 32 columns
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                *reinterpret_cast<float4*>(so + (x / 32) * kAtom + r * 128 + (((y + (x & 16) / 4) ^ (r & 7)) << 4)) =
+                            for (int y = 0; y < 8; ++y)
+                                *reinterpret_cast<float4*>(so + (x / 32) * kAtom + ((y ^ (r & 7)) << 4)) =
                                     make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
                         } else {                                   // tiles of 64
 #pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                *reinterpret_cast<uint4*>(so + (x / 64) * kAtom + r * 128 + (((y + (x & 48) / 8) ^ (r & 7)) << 4)) =
+                            for (int y = 0; y < 4; ++y)
+                                *reinterpret_cast<uint4*>(so + (x / 64) * kAtom + (((y + (x & 32) / 8) ^ (r & 7)) << 4)) =
                                     make_uint4(pack_bf16x2(v[8 * y], v[8 * y + 1]), pack_bf16x2(v[8 * y + 2], v[8 * y + 3]),
                                                pack_bf16x2(v[8 * y + 4], v[8 * y + 5]), pack_bf16x2(v[8 * y + 6], v[8 * y + 7]));
                         }
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         for (int id = tid; id < n * chunks; id += 128) {
                             const int rr = id / chunks, ch = id % chunks;
                             *reinterpret_cast<uint4*>(dst + ((row + rr) * s.o_ld + (int64_t)wk->head * DV) * es + ch * 16) =
-                                *reinterpret_cast<const uint4*>(so + (ch >> 3) * kAtom + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                                *reinterpret_cast<const uint4*>(so + (ch >> 3) * kAtom + (rr - r) * 128 + (((ch & 7) ^ (rr & 7)) << 4));
                         }
                     }
                     fence_async_smem();
@@ -491,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         }
     } else if (warp < 8) {
         // ------------------------------------------------------------------ the state
-        regs_up<STATES ? kRegsStateOnly : kRegsState>();
+        regs_up<kRegsState>();
         const int d = tid - 128;                                   // state row = TMEM lane
         const uint32_t lanes = tmem + ((uint32_t)((warp - 4) * 32) << 16);
         const bool mine = d < DV;
@@ -578,169 +590,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     } else {
         // ------------------------------------------------------------------ one warp each
         regs_down<kRegsCtl>();
-        if (warp == 12) {                                          // loads
-            int i = 0;
-            for (int k = 0;; ++k) {
-                const Work* wk = open(k, 0, 32);
-                if (!wk) break;
-                if (lane == 0) {
-                    const LinearScan& s = a.s[wk->scan];
-                    const ScanMaps& m = maps.m[wk->scan];
-                    const int nb = (wk->n + kB - 1) / kB, h = wk->head;
-                    const int cq = h / s.q_share * DK, ck = h / s.k_share * DK, cv = h / s.v_share * DV;
-                    for (int x0 = 0; x0 < nb; ++x0, ++i) {
-                        const int st = i % C::kStages;
-                        const uint32_t dst = sb + (uint32_t)st * C::kStage;
-                        const int row = wk->row0 + block(s.reverse, nb, x0) * kB;
-                        if (i >= C::kStages) wait(kv_empty(st), i / C::kStages - 1);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(kv_full(st), C::kK + C::kV);
-                        for (int x = 0; x < DV / 64; ++x)
-                            tma_load_3d(dst + C::kQ + C::kK + x * kAtom, &m.v, cv + 64 * x, row, 0, kv_full(st));
-                        for (int x = 0; x < DK / 64; ++x)
-                            tma_load_3d(dst + C::kQ + x * kAtom, &m.k, ck + 64 * x, row, 0, kv_full(st));
-                        if constexpr (!STATES) {
-                            if (i >= C::kStages) wait(q_empty(st), i / C::kStages - 1);
-                            if (!ok) break;
-                            mbar_arrive_expect_tx(q_full(st), C::kQ);
-                            for (int x = 0; x < DK / 64; ++x)
-                                tma_load_3d(dst + x * kAtom, &m.q, cq + 64 * x, row, 0, q_full(st));
-                        }
-                    }
-                }
-                close(k);
-            }
-            // nothing is in flight when the block ends, whatever gave up
-            if (lane == 0)
-                for (int x = max(0, i - C::kStages); x < i; ++x) {
-                    mbar_wait_bounded(kv_full(x % C::kStages), (uint32_t)(x / C::kStages & 1), kWait);
-                    if (!STATES) mbar_wait_bounded(q_full(x % C::kStages), (uint32_t)(x / C::kStages & 1), kWait);
-                }
-        } else if (warp == 13) {                                   // MMAs: the warp waits, one lane issues
-            const bool leader = elect_one();
-            int i = 0;
-            for (int k = 0;; ++k) {
-                const Work* wk = open(k, 0, 32);
-                if (!wk) break;
-                // o is staged over Q's tiles; k's and v's are free as soon as the block's MMAs are done,
-                // unless o is larger than q
-                const bool kv_early = STATES || (DV <= DK && !a.s[wk->scan].o_f32);
-                const int nb = (wk->n + kB - 1) / kB;
-                close(k);
-                for (int x0 = 0; x0 < nb; ++x0, ++i) {
-                    const int st = i % C::kStages;
-                    const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK, ss = sb + C::kOffS;
-                    // descriptors count addresses in 16 bytes
-                    const uint64_t kmn = sdesc_sw128_mn(sk);
-                    wait(kv_full(st), i / C::kStages);
-                    if (!STATES) wait(q_full(st), i / C::kStages);
-                    fence_after_sync();
-                    if constexpr (!STATES) {
-                        const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), sd = sdesc_sw128(ss);
-                        if (leader) {
-#pragma unroll
-                            for (int x = 0; x < DK / 16; ++x) {
-                                const uint64_t at = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
-                                mma_bf16(tmem + kColP, qd + at, kd + at, idesc_bf16(128, 128, 0, 0), x > 0);
-                            }
-                            mma_commit(qk_done);
-                        }
-                        __syncwarp();
-                        wait(s_ready, i);
-                        if (i > 0) wait(o_free, i - 1);
-                        fence_after_sync();
-                        if (leader) {
-#pragma unroll
-                            for (int x = 0; x < DK / 16; ++x)
-                                mma_bf16(tmem + kColO, qd + (((x >> 2) * kAtom + (x & 3) * 32) >> 4),
-                                         sd + (((x >> 2) * (DV * 128) + (x & 3) * 32) >> 4), idesc_bf16(128, DV, 0, 0), x > 0);
-                            mma_commit(inter_done);
-                        }
-                        __syncwarp();
-                    }
-                    if (i > 0) wait(u_free, i - 1);
-#pragma unroll 1
-                    for (int u = 0; u < kB / kSub; ++u) {
-                        const int kk = i * (kB / kSub) + u;
-                        wait(v_ready(kk & 1), kk >> 1);
-                        fence_after_sync();
-                        const uint32_t at = tmem + kColV + (uint32_t)(kk & 1) * kSlotCols;
-                        if (leader) {
-#pragma unroll
-                            for (int x = 0; x < kSub / 16; ++x)
-#pragma unroll
-                                for (int t = 0; t < 3; ++t)
-                                    mma_bf16_ts(tmem + kColU, at + t * 16 + x * 8, kmn + (uint64_t)((u * kSub + x * 16) * 128 >> 4),
-                                                idesc_bf16(128, DK, 0, 1), u + x + t > 0);
-                            mma_commit(v_free(kk & 1));
-                            if (u == kB / kSub - 1) {
-                                mma_commit(u_done);
-                                if (STATES) mma_commit(kv_empty(st));
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    if constexpr (!STATES) {
-                        wait(p_ready, i);
-                        wait(inter_read, i);
-                        fence_after_sync();
-                        const uint64_t vmn = sdesc_sw128_mn(sv);
-                        if (leader) {
-#pragma unroll
-                            for (int x = 0; x < kB / 16; ++x)
-                                mma_bf16_ts(tmem + kColO, tmem + kColP + x * 8, vmn + (uint64_t)(x * 2048 >> 4), idesc_bf16(128, DV, 0, 1), x > 0);
-                            mma_commit(intra_done);
-                            if (kv_early) mma_commit(kv_empty(st));
-                        }
-                        __syncwarp();
-                    }
-                }
-            }
-            if (i > 0) {
-                mbar_wait_bounded(u_done, (uint32_t)((i - 1) & 1), kWait);
-                if (!STATES) mbar_wait_bounded(intra_done, (uint32_t)((i - 1) & 1), kWait);
-            }
-        } else if (warp == 14 && !STATES) {                        // stores
-            int i = 0;
-            for (int k = 0;; ++k) {
-                const Work* wk = open(k, 0, 32);
-                if (!wk) break;
-                if (lane == 0) {
-                    const LinearScan& s = a.s[wk->scan];
-                    const CUtensorMap* m = &maps.m[wk->scan].o;
-                    const bool kv_early = DV <= DK && !s.o_f32;
-                    const int per = s.o_f32 ? 32 : 64, nb = (wk->n + kB - 1) / kB, c0 = wk->head * DV;
-                    for (int x0 = 0; x0 < nb; ++x0, ++i) {
-                        const int st = i % C::kStages, b = block(s.reverse, nb, x0);
-                        wait(o_staged, i);
-                        if (tokens(wk->n, b) == kB) {
-                            for (int x = 0; x < DV / per; ++x)
-                                tma_store_3d(m, sb + (uint32_t)st * C::kStage + x * kAtom, c0 + per * x, wk->row0 + b * kB, 0);
-                            bulk_commit();
-                            bulk_wait_read_all();
-                        }
-                        mbar_arrive_local(q_empty(st));
-                        if (!kv_early) mbar_arrive_local(kv_empty(st));
-                    }
-                }
-                close(k);
-            }
-            if (lane == 0) bulk_wait_all();
-        } else if (warp == 15) {                                   // the list of segments
+        if (warp == 16) {                                          // the list of segments, and their loads
             const int64_t total = c.items * c.H * a.nscans;
-            int k = 0;
-            for (int64_t w = blockIdx.x;; w += gridDim.x) {
-                const bool end = w >= total;
+            int64_t w = blockIdx.x;
+            // the CTA's k-th segment into its slot; false after the last
+            auto list = [&](int k) {
                 LinearItem it{};
-                const int z = (int)(w % a.nscans);
-                const int64_t ih = w / a.nscans;
-                const int h = (int)(ih % c.H);
-                const bool rev = a.s[z].reverse;
-                if (!end) {
-                    if (!linear_item(c, ih / c.H, &it)) continue;
+                int z = 0, h = 0;
+                bool rev = false;
+                for (;; w += gridDim.x) {
+                    if (w >= total) break;
+                    z = (int)(w % a.nscans);
+                    h = (int)(w / a.nscans % c.H);
+                    rev = a.s[z].reverse;
+                    if (!linear_item(c, w / a.nscans / c.H, &it)) continue;
                     if (STATES && (rev ? it.seg == 0 : it.seg == it.nseg - 1)) continue;   // nothing follows it
+                    break;
                 }
+                const bool end = w >= total;
                 if (k >= 2) wait(w_empty(k & 1), (k >> 1) - 1);
+                ok = __all_sync(0xffffffffu, ok);
                 Work* wk = works + (k & 1);
                 if (!end) {
                     // l^e in fp32: g e as the sum of a product and its rounding error
@@ -758,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         wk->scan = z;
                         wk->head = h;
                         wk->slot = (int)it.slot;
-                        wk->item = (int)(ih / c.H);
+                        wk->item = (int)(w / a.nscans / c.H);
                         wk->flags = (linear_has_init(c, a.s[z], it.seq) ? kFirstInit : 0) | (it.nseg > 1 ? kSplit : 0) |
                                     ((rev ? it.seg == 0 : it.seg == it.nseg - 1) ? kFinal : 0);
                     }
@@ -766,16 +635,165 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (lane == 0) wk->n = end ? -1 : (int)it.n;
                 __syncwarp();
                 if (lane == 0) mbar_arrive_local(w_full(k & 1));
-                ++k;
-                if (end || !ok) break;
+                w += gridDim.x;
+                return !end && ok;
+            };
+            int i = 0;
+            for (int k = 0; list(k); ++k) {
+                if (lane == 0) {
+                    const Work* wk = works + (k & 1);
+                    const LinearScan& s = a.s[wk->scan];
+                    const ScanMaps& m = maps.m[wk->scan];
+                    const int nb = (wk->n + kB - 1) / kB, h = wk->head, row0 = wk->row0;
+                    const int cq = h / s.q_share * DK, ck = h / s.k_share * DK, cv = h / s.v_share * DV;
+                    for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                        const int st = i % C::kStages;
+                        const uint32_t dst = sb + (uint32_t)st * C::kStage;
+                        const int row = row0 + block(s.reverse, nb, x0) * kB;
+                        if (i >= C::kStages) wait(kv_empty(st), i / C::kStages - 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(kv_full(st), C::kK + C::kV);
+                        for (int x = 0; x < DV / 64; ++x)
+                            tma_load_3d(dst + C::kQ + C::kK + x * kAtom, &m.v, cv + 64 * x, row, 0, kv_full(st));
+                        for (int x = 0; x < DK / 64; ++x)
+                            tma_load_3d(dst + C::kQ + x * kAtom, &m.k, ck + 64 * x, row, 0, kv_full(st));
+                        if constexpr (!STATES) {
+                            if (i >= C::kStages) wait(q_empty(st), i / C::kStages - 1);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(q_full(st), C::kQ);
+                            for (int x = 0; x < DK / 64; ++x)
+                                tma_load_3d(dst + x * kAtom, &m.q, cq + 64 * x, row, 0, q_full(st));
+                        }
+                    }
+                }
+                __syncwarp();
             }
+            // nothing is in flight when the block ends, whatever gave up
+            if (lane == 0)
+                for (int x = max(0, i - C::kStages); x < i; ++x) {
+                    mbar_wait_bounded(kv_full(x % C::kStages), (uint32_t)(x / C::kStages & 1), kWait);
+                    if (!STATES) mbar_wait_bounded(q_full(x % C::kStages), (uint32_t)(x / C::kStages & 1), kWait);
+                }
+        } else if (warp == 17 && !STATES) {                        // MMAs of the outputs: the warp waits, one lane issues
+            const bool leader = elect_one();
+            int i = 0;
+            for (int k = 0;; ++k) {
+                const Work* wk = open(k, 0, 32);
+                if (!wk) break;
+                const int nb = (wk->n + kB - 1) / kB;
+                close(k);
+                for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                    const int st = i % C::kStages;
+                    const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK, ss = sb + C::kOffS;
+                    // descriptors count addresses in 16 bytes
+                    const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), sd = sdesc_sw128(ss), vmn = sdesc_sw128_mn(sv);
+                    wait(kv_full(st), i / C::kStages);
+                    wait(q_full(st), i / C::kStages);
+                    fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int x = 0; x < DK / 16; ++x) {
+                            const uint64_t at = ((x >> 2) * kAtom + (x & 3) * 32) >> 4;
+                            mma_bf16(tmem + kColP, qd + at, kd + at, idesc_bf16(128, 128, 0, 0), x > 0);
+                        }
+                        mma_commit(qk_done);
+                    }
+                    __syncwarp();
+                    wait(s_ready, i);
+                    if (i > 0) wait(o_free, i - 1);
+                    fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int x = 0; x < DK / 16; ++x)
+                            mma_bf16(tmem + kColO, qd + (((x >> 2) * kAtom + (x & 3) * 32) >> 4),
+                                     sd + (((x >> 2) * (DV * 128) + (x & 3) * 32) >> 4), idesc_bf16(128, DV, 0, 0), x > 0);
+                        mma_commit(inter_done);
+                    }
+                    __syncwarp();
+                    wait(p_ready, i);
+                    wait(inter_read, i);
+                    fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int x = 0; x < kB / 16; ++x)
+                            mma_bf16_ts(tmem + kColO, tmem + kColP + x * 8, vmn + (uint64_t)(x * 2048 >> 4), idesc_bf16(128, DV, 0, 1), 1);
+                        mma_commit(intra_done);
+                        if (a.early) mma_commit(kv_empty(st));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (i > 0) mbar_wait_bounded(intra_done, (uint32_t)((i - 1) & 1), kWait);
+        } else if (warp == 18 && !STATES) {                        // stores
+            int i = 0;
+            for (int k = 0;; ++k) {
+                const Work* wk = open(k, 0, 32);
+                if (!wk) break;
+                if (lane == 0) {
+                    const LinearScan& s = a.s[wk->scan];
+                    const CUtensorMap* m = &maps.m[wk->scan].o;
+                    const int per = s.o_f32 ? 32 : 64, nb = (wk->n + kB - 1) / kB, c0 = wk->head * DV;
+                    for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                        const int st = i % C::kStages, b = block(s.reverse, nb, x0);
+                        wait(o_staged, i);
+                        if (tokens(wk->n, b) == kB) {
+                            for (int x = 0; x < DV / per; ++x)
+                                tma_store_3d(m, sb + (uint32_t)st * C::kStage + x * kAtom, c0 + per * x, wk->row0 + b * kB, 0);
+                            bulk_commit();
+                            bulk_wait_read_all();
+                        }
+                        mbar_arrive_local(q_empty(st));
+                        if (!a.early) mbar_arrive_local(kv_empty(st));
+                    }
+                }
+                close(k);
+            }
+            if (lane == 0) bulk_wait_all();
+        } else if (warp == 19) {                                   // MMAs of the state, whenever their operands are there
+            const bool leader = elect_one();
+            int i = 0;
+            for (int k = 0;; ++k) {
+                const Work* wk = open(k, 0, 32);
+                if (!wk) break;
+                const int nb = (wk->n + kB - 1) / kB;
+                close(k);
+                for (int x0 = 0; x0 < nb; ++x0, ++i) {
+                    const int st = i % C::kStages;
+                    const uint64_t kmn = sdesc_sw128_mn(sb + (uint32_t)st * C::kStage + C::kQ);
+                    wait(kv_full(st), i / C::kStages);
+                    if (i > 0) wait(u_free, i - 1);
+                    if (!STATES && !a.early && i > 0) wait(o_free, i - 1);
+#pragma unroll 1
+                    for (int u = 0; u < kB / kSub; ++u) {
+                        const int kk = i * (kB / kSub) + u;
+                        wait(v_ready(kk & 1), kk >> 1);
+                        fence_after_sync();
+                        const uint32_t at = tmem + kColV + (uint32_t)(kk & 1) * kSlotCols;
+                        if (leader) {
+#pragma unroll
+                            for (int x = 0; x < kSub / 16; ++x)
+#pragma unroll
+                                for (int t = 0; t < 3; ++t)
+                                    mma_bf16_ts(tmem + kColU, at + t * 16 + x * 8, kmn + (uint64_t)((u * kSub + x * 16) * 128 >> 4),
+                                                idesc_bf16(128, DK, 0, 1), u + x + t > 0);
+                            mma_commit(v_free(kk & 1));
+                            if (u == kB / kSub - 1) {
+                                mma_commit(u_done);
+                                mma_commit(kv_empty(st));
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (i > 0) mbar_wait_bounded(u_done, (uint32_t)((i - 1) & 1), kWait);
         }
     }
     if (!ok) set_device_status(c.status, kDevTimeout);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (warp == 13) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -850,10 +868,12 @@ cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int n
         TcMaps m;
         memset(&m, 0, sizeof(m));
         a.c = c;
+        a.early = true;
         for (int j = i; j < nscans; ++j) {
             const LinearScan& s = scans[j];
             if (done[j] || s.DK != scans[i].DK || s.DV != scans[i].DV) continue;
             done[j] = true;
+            if (s.DV > s.DK || s.o_f32) a.early = false;
             a.s[a.nscans] = s;
             ScanMaps& x = m.m[a.nscans++];
             if (c.T > 0 && (!encode_rows(&x.q, s.q, c.T, (int64_t)(c.H / s.q_share) * s.DK, s.q_ld, false) ||
