@@ -157,20 +157,26 @@ template <int DK>
 __device__ __forceinline__ void load_state(const float* p, unsigned char* buf, int lane, float* S)
 {
     constexpr int kC = DK / 8;                    // 16-byte chunks of half a row
+    // all loads first, into the registers that the rows will take: one latency, not one for every few
+#pragma unroll
+    for (int x = 0; x < 2 * kC; ++x) {
+        const int at = (x % kC) * 32 + lane, r = at / kC, ch = at % kC;
+        const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)r * DK + (x / kC) * (DK / 2) + ch * 4);
+        S[4 * x] = v.x; S[4 * x + 1] = v.y; S[4 * x + 2] = v.z; S[4 * x + 3] = v.w;
+    }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-#pragma unroll 4
-        for (int x = lane; x < 32 * kC; x += 32) {
-            const int r = x / kC, ch = x % kC;
-            const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)r * DK + half * (DK / 2) + ch * 4);
-            *reinterpret_cast<float4*>(buf + r * (DK * 2) + ((ch ^ (r & 7)) << 4)) = v;
+        float* o = S + half * (DK / 2);
+#pragma unroll
+        for (int x = 0; x < kC; ++x) {
+            const int at = x * 32 + lane, r = at / kC, ch = at % kC;
+            *reinterpret_cast<float4*>(buf + r * (DK * 2) + ((ch ^ (r & 7)) << 4)) = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
         __syncwarp();
 #pragma unroll
         for (int ch = 0; ch < kC; ++ch) {
             const float4 v = *reinterpret_cast<const float4*>(buf + lane * (DK * 2) + ((ch ^ (lane & 7)) << 4));
-            float* o = S + half * (DK / 2) + ch * 4;
-            o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+            o[4 * ch] = v.x; o[4 * ch + 1] = v.y; o[4 * ch + 2] = v.z; o[4 * ch + 3] = v.w;
         }
         __syncwarp();
     }
