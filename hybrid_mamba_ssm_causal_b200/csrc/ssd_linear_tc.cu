@@ -31,7 +31,7 @@
 // kept rolled where registers allow: the warpgroups' code competes for the instruction cache. Nothing may spill: beside 227 KB of shared
 // memory the L1 has some 16 KB left.
 //
-// No decay factor is ever above 1: off the diagonal 32 x 32 tiles, l^{i-j} = l^{i-j0-31} l^{31-(j-j0)}.
+// No decay factor is ever above 1: every score is multiplied by its own l^{i-j}, from a table.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -66,18 +66,17 @@ struct Cfg {
     static constexpr uint32_t kQ = STATES ? 0 : kAtom * (DK / 64), kK = kAtom * (DK / 64), kV = kAtom * (DV / 64);
     static constexpr uint32_t kStage = kQ + kK + kV;
     static constexpr uint32_t kS = DV * DK * 2;  // operand copy of S; staging of whole states
-    static constexpr uint32_t kTail = 2048;      // the segments' powers and places, barriers
+    static constexpr uint32_t kTail = 2560;      // the segments' powers and places, barriers
     static constexpr int kFit = (int)((kSmemMax - kS - kTail) / kStage);
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static_assert(kStages >= 2, "two stages");
-    static constexpr uint32_t kOffS = kStages * kStage, kOffWork = kOffS + kS, kOffBar = kOffWork + 2 * 720;
+    static constexpr uint32_t kOffS = kStages * kStage, kOffWork = kOffS + kS, kOffBar = kOffWork + 2 * 1072;
     static constexpr uint32_t kSmem = kOffWork + kTail;
 };
 
 // One segment of one scan, as the list warp leaves it for the others.
 struct Work {
-    float tab[132];      // l^0 .. l^128
-    float wtab[32];      // l^{31-x} (backwards l^x)
+    float pow[256];      // l^{|e - 127|}
     float log_l;
     int n;               // tokens; -1: the list has ended
     int row0, scan, head, slot;
@@ -85,7 +84,7 @@ struct Work {
     int item;            // seg_states index
 };
 enum : int { kFirstInit = 1, kSplit = 2, kFinal = 4 };   // from an initial state; one of several segments; the scan's last
-static_assert(sizeof(Work) <= 720, "room for two");
+static_assert(sizeof(Work) <= 1072, "room for two");
 
 struct ScanMaps {
     CUtensorMap q, k, v, o;
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             const int j = j0 + 8 * x, e = rev ? j + 1 : n - 1 - j, e1 = rev ? j + 2 : n - 2 - j;
-                            w[x] = make_float2(us * wk->tab[max(e, 0)], us * wk->tab[max(e1, 0)]);
+                            w[x] = make_float2(us * wk->pow[127 + max(e, 0)], us * wk->pow[127 + max(e1, 0)]);
                         }
                         // addresses: matrix m = lane / 8 is token group m, its row lane % 8 a token
                         const uint32_t row = (uint32_t)(u * kSub + lane);
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const LinearScan& s = a.s[wk->scan];
                 const bool rev = s.reverse, o_f32 = s.o_f32;
                 const float out_scale = s.out_scale, ps = s.out_scale * s.u_scale;
-                const float* tab = wk->tab;
+                const float* tab = wk->pow + 127;                 // l^{|e|}
                 const int nall = wk->n, nb = (nall + kB - 1) / kB;
                 for (int x0 = 0; x0 < nb; ++x0, ++i) {
                     const int st = i % C::kStages;
@@ -398,41 +397,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     fence_after_sync();
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {                  // 32 score columns at a time
+                        float v[32];
+                        tmem_ld32(lanes + kColP + 32 * m, v);
+                        // columns x <= g forwards, x >= g that are tokens backwards, times c u l^{|g - x|}: one code
+                        // for every tile and direction
+                        const int g = r - 32 * m, left = n - 32 * m;
+                        const uint32_t from = g <= 0 ? 0xffffffffu : (g < 32 ? 0xffffffffu << g : 0u);       // x >= g
+                        const uint32_t to = g < 0 ? 0u : (g < 31 ? (2u << g) - 1u : 0xffffffffu);             // x <= g
+                        const uint32_t in = left <= 0 ? 0u : (left < 32 ? (1u << left) - 1u : 0xffffffffu);
+                        const uint32_t mask = rev ? from & in : to;
+                        const float* t = tab + g;
                         uint32_t p[16];
-                        if (rev ? m < warp : m > warp) {           // all outside the mask
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) p[x] = 0;
-                        } else {
-                            float v[32];
-                            tmem_ld32(lanes + kColP + 32 * m, v);
-                            tmem_wait_ld();
-                            if (m == warp) {
-#pragma unroll
-                                for (int x = 0; x < 32; ++x) {
-                                    const float t = v[x] * (ps * tab[rev ? max(x - lane, 0) : max(lane - x, 0)]);
-                                    v[x] = (rev ? x >= lane : x <= lane) ? t : 0.0f;
-                                }
-                            } else {
-                                const float2 f = splat2(ps * tab[rev ? 32 * m - r : r - 32 * m - 31]);
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) {
-                                    const float4 t = reinterpret_cast<const float4*>(wk->wtab)[x];
-                                    const float2 t0 = mul2(mul2(f, make_float2(t.x, t.y)), make_float2(v[4 * x], v[4 * x + 1]));
-                                    const float2 t1 = mul2(mul2(f, make_float2(t.z, t.w)), make_float2(v[4 * x + 2], v[4 * x + 3]));
-                                    v[4 * x] = t0.x;
-                                    v[4 * x + 1] = t0.y;
-                                    v[4 * x + 2] = t1.x;
-                                    v[4 * x + 3] = t1.y;
-                                }
-                            }
-                            const int left = n - 32 * m;           // columns that are tokens
-                            if (left < 32) {
-#pragma unroll
-                                for (int x = 0; x < 32; ++x) v[x] = x < left ? v[x] : 0.0f;
-                            }
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+                        for (int x = 0; x < 32; ++x) {
+                            const float y = v[x] * t[-x];
+                            v[x] = mask >> x & 1u ? y : 0.0f;
                         }
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) p[x] = pack_f2(mul2(splat2(ps), make_float2(v[2 * x], v[2 * x + 1])));
                         tmem_st16(lanes + kColP + 16 * m, p);
                     }
                     if (n < kB) {     // P's zeros must not meet what rows behind the sequence hold
@@ -625,8 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         return expf(p) * (1.0f + fmaf(g, (float)e, -p));
                     };
 #pragma unroll 1
-                    for (int e = lane; e <= kB; e += 32) wk->tab[e] = power(e);
-                    wk->wtab[lane] = power(rev ? lane : 31 - lane);
+                    for (int e = lane; e < 256; e += 32) wk->pow[e] = power(abs(e - 127));
                     if (lane == 0) {
                         wk->log_l = g;
                         wk->row0 = (int)it.row0;
