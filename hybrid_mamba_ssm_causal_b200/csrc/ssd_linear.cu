@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     constexpr int kPer = (kTileVecs + kThr - 1) / kThr;
     __shared__ __align__(16) T s_in[kTile][2 * DK + DV];      // k, then q, then v
     __shared__ __align__(16) float s_o[kTile][DV];
+    if (c.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *c.status = kDevOk;
 
     const int h = blockIdx.x % c.H;
     const int64_t item = blockIdx.x / c.H;
@@ -216,32 +217,64 @@ void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, cudaStrea
 
 // ------------------------------------------------------------- states between segments
 // Rows of one segment are left alone. Before: seg_states[t] holds segment t's own state from a zero
-// start (the last segment of the scan has none). After: the state entering segment t.
+// start (the last segment of the scan has none). After: the state entering segment t. A block takes
+// 4096 elements of one (sequence, head); a thread's loads of the next segment are under way while one
+// is added.
+constexpr int kPassElems = 4096;
 __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, const LinearScan s)
 {
+    __shared__ LinearItem first;
+    __shared__ int64_t item0;
     const int h = blockIdx.y;
     const int64_t seq = blockIdx.z;
-    const int hs = s.DK * s.DV;
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    int64_t item0 = seq * c.nseg;
-    if (c.cu_seqlens) {
-        int64_t start = c.cu_seqlens[seq];
-        start = start < 0 ? 0 : (start > c.T ? c.T : start);
-        item0 = seq + start / c.seg_tokens;
+    const int hs = s.DK * s.DV, e0 = blockIdx.x * kPassElems + 4 * threadIdx.x;
+    if (threadIdx.x == 0) {
+        int64_t i0 = seq * c.nseg;
+        if (c.cu_seqlens) {
+            int64_t start = c.cu_seqlens[seq];
+            start = start < 0 ? 0 : (start > c.T ? c.T : start);
+            i0 = seq + start / c.seg_tokens;
+        }
+        item0 = i0;
+        if (!linear_item(c, i0, &first) || first.seq != seq || i0 + first.nseg > c.items) first.nseg = 0;
     }
-    LinearItem it;
-    if (i >= hs || !linear_item(c, item0, &it) || it.nseg < 2) return;
-    const int d = i / s.DK, e = i - d * s.DK;
+    __syncthreads();
+    const int64_t nseg = first.nseg;
+    if (nseg < 2) return;
     const float g = linear_log_decay(c.log_decay, h);
-    float S = linear_has_init(c, s, seq) ? s.init[(it.slot * c.H + h) * (int64_t)hs + (int64_t)d * s.init_rs + (int64_t)e * s.init_cs] : 0.0f;
-    for (int64_t k = 0; k < it.nseg; ++k) {
-        const int64_t t = s.reverse ? it.nseg - 1 - k : k;
-        LinearItem seg;
-        if (!linear_item(c, item0 + t, &seg)) return;
-        float* p = s.seg_states + ((item0 + t) * c.H + h) * (int64_t)hs + i;
-        const float own = k + 1 < it.nseg ? *p : 0.0f;
-        *p = S;
-        S = LinearDecay(g * (float)seg.n).step(S, own);
+    const bool init = linear_has_init(c, s, seq);
+    const float* ip = s.init ? s.init + (first.slot * c.H + h) * (int64_t)hs : nullptr;
+    // segments in scan order; the short one is the row's last
+    auto at = [&](int64_t k) { return s.seg_states + ((item0 + (s.reverse ? nseg - 1 - k : k)) * c.H + h) * (int64_t)hs; };
+    constexpr int kV = kPassElems / 1024;
+    float4 S[kV], own[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int i = e0 + v * 1024;
+        S[v] = own[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i >= hs) continue;
+        own[v] = *reinterpret_cast<const float4*>(at(0) + i);
+        if (init) {
+            const float* p = ip + (int64_t)(i / s.DK) * s.init_rs + (int64_t)(i % s.DK) * s.init_cs;   // four of one row
+            S[v] = make_float4(p[0], p[s.init_cs], p[2 * s.init_cs], p[3 * s.init_cs]);
+        }
+    }
+    const LinearDecay whole(g * (float)c.seg_tokens);
+    for (int64_t k = 0; k < nseg; ++k) {
+        float4 next[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            next[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (e0 + v * 1024 < hs && k + 2 < nseg) next[v] = *reinterpret_cast<const float4*>(at(k + 1) + e0 + v * 1024);
+        }
+        // backwards the short segment comes first (only fixed-length rows run backwards)
+        const LinearDecay d = s.reverse && k == 0 ? LinearDecay(g * (float)(c.L - (nseg - 1) * c.seg_tokens)) : whole;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            if (e0 + v * 1024 < hs) *reinterpret_cast<float4*>(at(k) + e0 + v * 1024) = S[v];
+            S[v] = make_float4(d.step(S[v].x, own[v].x), d.step(S[v].y, own[v].y), d.step(S[v].z, own[v].z), d.step(S[v].w, own[v].w));
+            own[v] = next[v];
+        }
     }
 }
 
@@ -355,7 +388,10 @@ void launch_decode(const LinearDecode& p, int DK, int64_t b, cudaStream_t st)
 cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStream_t st)
 {
     if (c.items == 0) return cudaSuccess;
+    LinearCall call = c;
     const auto run = [&](bool state_only) {
+        const LinearCall c = call;
+        call.clear_status = false;
         if (c.act == SSD_BF16) launch_scan_dk<__nv_bfloat16>(c, s, state_only, st);
         else launch_scan_dk<float>(c, s, state_only, st);
         return cudaGetLastError();
@@ -372,7 +408,7 @@ cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStr
 cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st)
 {
     LaunchScope ls("linear_pass", st);
-    linear_pass_kernel<<<dim3((unsigned)((s.DK * s.DV + 255) / 256), (unsigned)c.H, (unsigned)c.b), 256, 0, st>>>(c, s);
+    linear_pass_kernel<<<dim3((unsigned)((s.DK * s.DV + kPassElems - 1) / kPassElems), (unsigned)c.H, (unsigned)c.b), 256, 0, st>>>(c, s);
     return cudaGetLastError();
 }
 
@@ -387,24 +423,29 @@ int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool pac
     const double start = tc ? 0.8 : 1.5, states = tc ? 0.5 : 0.6, join = tc ? 2.0 : 3.0, each = tc ? 0.01 : 0.02;
     const int64_t blocks = ((packed ? T : L) + 127) / 128;
     if (blocks <= 1 || b == 0) return 256;                 // nothing to split: longer than any row
-    // a packed row's length is not known here; they are taken as equal, and each may end in part of a segment
-    const int64_t per_row = packed ? (blocks + b - 1) / b : blocks;
+    if (packed && b > 1) {
+        // The lengths are not known here. Segments are twice an SM's even share of all blocks (and 8 at
+        // least): shorter rows, which find their place among the others, stay whole, and one long prompt
+        // among many short rows does not keep a few SMs busy alone.
+        const int64_t share = (blocks * H * nscans + slots - 1) / slots;
+        return (2 * share > 8 ? 2 * share : 8) * 128;
+    }
+    const int64_t per_row = blocks;
     double best = 0.0;
     int64_t best_seg = 0;
     for (int64_t nseg = 1; nseg <= per_row && nseg <= 256; ++nseg) {
         const int64_t seg = (per_row + nseg - 1) / nseg;
         if (best_seg && seg == best_seg) continue;
-        const int64_t n = packed ? (int64_t)H * nscans * (blocks / seg + (b + 1) / 2) : rows * ((per_row + seg - 1) / seg);
+        const int64_t n = rows * ((per_row + seg - 1) / seg);
         double cost = (double)((n + slots - 1) / slots) * (seg + start);
         if (seg < per_row)
-            cost += (double)((n - rows > 0 ? n - rows + slots - 1 : slots) / slots) * (states * seg + start) + join + each * (double)n * 148.0 / (double)sms;
+            cost += (double)((n - rows + slots - 1) / slots) * (states * seg + start) + join + each * (double)n * 148.0 / (double)sms;
         if (!best_seg || cost < best) {
             best = cost;
             best_seg = seg;
         }
     }
-    if (best_seg >= per_row && (!packed || b == 1)) return (blocks + 1) * 128;
-    return best_seg * 128;
+    return (best_seg >= per_row ? blocks + 1 : best_seg) * 128;
 }
 
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,

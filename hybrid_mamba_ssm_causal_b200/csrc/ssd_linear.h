@@ -46,7 +46,14 @@ struct LinearCall {
     // of a fixed-length one.
     int64_t seg_tokens, nseg, items;
     bool split;          // some row may have more than one segment
+    // 256 bytes at the start of the workspace: the status word, and (tensor cores, more segments than
+    // SMs) how many segments the CTAs of the states' and of the main pass have taken beyond their first.
+    // Those calls clear all of it beforehand; others leave the status word to the first kernel's block 0,
+    // as it starts: a block can only set it seconds later, when a wait gives up, or at its start for the
+    // reason that block 0 meets too.
     int* status;
+    int* taken;
+    bool clear_status;
 };
 
 // Longest supported per-call counts keep every index in 32-bit grid dimensions.

@@ -116,8 +116,11 @@ ssd_status run(const ssd::LinearCall& c, const ssd::LinearScan* s, int n, cudaSt
 {
     if (ssd::linear_tc_supported(s[0], c.act))
         return ssd::launch_linear_tc(c, s, n, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
-    for (int i = 0; i < n; ++i)
-        if (ssd::launch_linear_simt(c, s[i], st) != cudaSuccess) return SSD_ERR_CUDA;
+    ssd::LinearCall call = c;
+    for (int i = 0; i < n; ++i) {
+        if (ssd::launch_linear_simt(call, s[i], st) != cudaSuccess) return SSD_ERR_CUDA;
+        call.clear_status = false;
+    }
     return SSD_OK;
 }
 
@@ -174,7 +177,8 @@ ssd_status ssd_mixer_linear_prefill(const ssd_linear_dims* d, const void* q, int
     c.nslots = d->batch;
     c.status = (int*)workspace;
     cudaStream_t st = (cudaStream_t)stream;
-    if (ssd::clear_device_status(c.status, st) != cudaSuccess) return SSD_ERR_CUDA;
+    c.taken = c.status + 1;
+    c.clear_status = true;
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, init_state, o, o_ld, final_state, (char*)workspace, w);
     return run(c, &s, 1, st);
 }
@@ -209,7 +213,8 @@ ssd_status ssd_mixer_linear_prefill_varlen(const ssd_linear_dims* d, const int32
     c.nslots = nslots;
     c.status = (int*)workspace;
     cudaStream_t st = (cudaStream_t)stream;
-    if (ssd::clear_device_status(c.status, st) != cudaSuccess) return SSD_ERR_CUDA;
+    c.taken = c.status + 1;
+    c.clear_status = true;
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, state, o, o_ld, state, (char*)workspace, w);
     return run(c, &s, 1, st);
 }
@@ -304,7 +309,8 @@ ssd_status ssd_mixer_linear_backward(const ssd_linear_dims* d, const void* q, in
         sk.o = ws + w.part_k; sk.o_ld = HK; sk.o_f32 = true;
     }
     for (int i = 0; i < 3; ++i) s[i].seg_states = (float*)(ws + w.seg + i * w.seg_each);
-    if (ssd::clear_device_status(c.status, st) != cudaSuccess) return SSD_ERR_CUDA;
+    c.taken = c.status + 1;
+    c.clear_status = true;
     const ssd_status rs = run(c, s, 3, st);
     if (rs != SSD_OK || r == 1) return rs;
     if (ssd::launch_linear_group_sum((const float*)(ws + w.part_k), dk, dk_ld, c.T, d->ngroups, r, d->dk, d->act, st) != cudaSuccess ||

@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const LinearCall& c = a.c;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the compiler sees
     const uint32_t sb = smem_u32(smem);
+    if (c.clear_status && blockIdx.x == 0 && tid == 0) *c.status = kDevOk;
     if (sb & 1023u) {
         if (tid == 0) set_device_status(c.status, kDevSmemMisaligned);
         return;
@@ -582,12 +583,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if (warp == 16) {                                          // the list of segments, and their loads
             const int64_t total = c.items * c.H * a.nscans;
             int64_t w = blockIdx.x;
+            // The CTA's next segment: its first, then whichever no CTA has taken (lengths differ).
+            auto next = [&]() {
+                int64_t t = total;
+                if (gridDim.x < total) {
+                    if (lane == 0) t = (int64_t)gridDim.x + atomicAdd(c.taken + (STATES ? 0 : 1), 1);
+                    t = __shfl_sync(0xffffffffu, t, 0);
+                }
+                return t;
+            };
             // the CTA's k-th segment into its slot; false after the last
             auto list = [&](int k) {
                 LinearItem it{};
                 int z = 0, h = 0;
                 bool rev = false;
-                for (;; w += gridDim.x) {
+                for (;; w = next()) {
                     if (w >= total) break;
                     z = (int)(w % a.nscans);
                     h = (int)(w / a.nscans % c.H);
@@ -623,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (lane == 0) wk->n = end ? -1 : (int)it.n;
                 __syncwarp();
                 if (lane == 0) mbar_arrive_local(w_full(k & 1));
-                w += gridDim.x;
+                if (!end) w = next();
                 return !end && ok;
             };
             int i = 0;
@@ -835,6 +845,9 @@ cudaError_t launch_shape(const TcArgs& a, const TcMaps& m, cudaStream_t st)
         cudaError_t e = launch_one<DK, DV, true>(a, m, st);
         for (int i = 0; i < a.nscans && e == cudaSuccess; ++i) e = launch_linear_pass(a.c, a.s[i], st);
         if (e != cudaSuccess) return e;
+        TcArgs after = a;
+        after.c.clear_status = false;
+        return launch_one<DK, DV, false>(after, m, st);
     }
     return launch_one<DK, DV, false>(a, m, st);
 }
@@ -849,6 +862,7 @@ bool linear_tc_supported(const LinearScan& s, int act)
 cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st)
 {
     if (c.items == 0) return cudaSuccess;
+    const bool queue = c.items * c.H * nscans > device_sm_count();   // of any launch below
     bool done[kMaxScans] = {};
     for (int i = 0; i < nscans; ++i) {   // scans of one shape run in the same launches
         if (done[i]) continue;
@@ -856,6 +870,12 @@ cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int n
         TcMaps m;
         memset(&m, 0, sizeof(m));
         a.c = c;
+        a.c.clear_status = c.clear_status && !queue && i == 0;
+        if (queue) {
+            a.c.taken = c.taken + 2 * i;
+            const cudaError_t e = i > 0 ? cudaSuccess : cudaMemsetAsync(c.status, 0, 256, st);
+            if (e != cudaSuccess) return e;
+        }
         a.early = true;
         for (int j = i; j < nscans; ++j) {
             const LinearScan& s = scans[j];
