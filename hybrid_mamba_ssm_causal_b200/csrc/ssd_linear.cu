@@ -228,15 +228,11 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
     const int h = blockIdx.y;
     const int64_t seq = blockIdx.z;
     const int hs = s.DK * s.DV, e0 = blockIdx.x * kPassElems + 4 * threadIdx.x;
+    if (c.cu_seqlens && (int64_t)c.cu_seqlens[seq + 1] - c.cu_seqlens[seq] <= c.seg_tokens) return;
     if (threadIdx.x == 0) {
-        int64_t i0 = seq * c.nseg;
-        if (c.cu_seqlens) {
-            int64_t start = c.cu_seqlens[seq];
-            start = start < 0 ? 0 : (start > c.T ? c.T : start);
-            i0 = seq + start / c.seg_tokens;
-        }
-        item0 = i0;
-        if (!linear_item(c, i0, &first) || first.seq != seq || i0 + first.nseg > c.items) first.nseg = 0;
+        item0 = c.cu_seqlens ? linear_packed_first(c, seq) : seq * c.nseg;
+        const bool is = c.cu_seqlens ? linear_packed_item(c, seq, 0, &first) : linear_item(c, item0, &first);
+        if (!is || item0 + first.nseg > c.items) first.nseg = 0;
     }
     __syncthreads();
     const int64_t nseg = first.nseg;
@@ -298,19 +294,72 @@ __global__ void __launch_bounds__(256) linear_group_sum_kernel(const float* __re
     o[0] = Act<T>::from_f(a.x); o[1] = Act<T>::from_f(a.y); o[2] = Act<T>::from_f(a.z); o[3] = Act<T>::from_f(a.w);
 }
 
-// ---------------------------------------------------------------------------- decode
-// One token a sequence, states in place: the fp32 state is read once and written once, which is
-// nearly all of the bytes. Lanes along DK (a float4 each), kRif state rows in flight per lane, so a
-// CTA's whole part of the state is on its way before the first product.
-constexpr int kDecodeThreads = 128, kRif = 8;
+// ------------------------------------------------------------------- lists of segments
+// One block: the packed call's segments, sorted by their blocks of 128 tokens (a counting sort, the
+// longest first, so that no CTA starts a long one last); those the recurrence does are left out. The
+// order of equals is left to chance: it decides which CTA takes which, not what is computed.
+constexpr int kListThreads = 1024, kBuckets = 256;
+__global__ void __launch_bounds__(kListThreads) linear_list_kernel(const LinearCall c)
+{
+    __shared__ int start[2][kBuckets];
+    if (threadIdx.x < 64) c.status[threadIdx.x] = 0;          // the status word, the counts, what is taken
+    for (int i = threadIdx.x; i < 2 * kBuckets; i += kListThreads) (&start[0][0])[i] = 0;
+    __syncthreads();
+    // bucket 0 holds the longest; z = 0: every segment, z = 1: those with one after them
+    const auto each = [&](auto use) {
+        for (int64_t seq = threadIdx.x; seq < c.b; seq += kListThreads) {
+            LinearItem it;
+            if (!linear_packed_item(c, seq, 0, &it) || (it.nseg == 1 && it.n <= kLinearShort)) continue;
+            for (int64_t seg = 0; seg < it.nseg; ++seg) {
+                linear_packed_item(c, seq, seg, &it);
+                const int64_t blocks = (it.n + 127) / 128;
+                const int bucket = kBuckets - 1 - (int)(blocks < kBuckets ? blocks : kBuckets - 1);
+                use(0, bucket, seq, seg);
+                if (seg + 1 < it.nseg) use(1, bucket, seq, seg);
+            }
+        }
+    };
+    each([&](int z, int bucket, int64_t, int64_t) { atomicAdd(&start[z][bucket], 1); });
+    __syncthreads();
+    if (threadIdx.x < 64) {                    // a warp per list, 8 buckets a lane: counts -> first places
+        const int z = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        int n[kBuckets / 32], own = 0;
+        for (int i = 0; i < kBuckets / 32; ++i) own += n[i] = start[z][lane * (kBuckets / 32) + i];
+        int sum = own;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) c.counts[z] = sum < c.items ? sum : (int)c.items;
+        sum -= own;
+        for (int i = 0; i < kBuckets / 32; ++i) {
+            start[z][lane * (kBuckets / 32) + i] = sum;
+            sum += n[i];
+        }
+    }
+    __syncthreads();
+    each([&](int z, int bucket, int64_t seq, int64_t seg) {
+        const int at = atomicAdd(&start[z][bucket], 1);
+        if (at < c.items) c.list[z * c.items + at] = make_int2((int)seq, (int)seg);
+    });
+}
 
-struct LinearDecode {
+// ---------------------------------------------------------------------------- decode and short rows
+// Up to kLinearShort tokens of each row, token by token: the fp32 state is read once and written once,
+// which for a few tokens is nearly all of the bytes. Lanes along DK (a float4 each), kRif state rows in
+// flight per lane, so a CTA's whole part of the state is on its way before the first product.
+// 256 sequences of 128 heads of 128 x 64: 341 us a step, 6.3 TB/s.
+constexpr int kShortThreads = 128, kRif = 8;
+
+struct LinearShort {
     const void *q, *k, *v;
     int64_t q_ld, k_ld, v_ld, o_ld;
     const float* log_decay;
-    float* state;
-    const int32_t* slot_idx;
-    int64_t nslots;
+    const float* init;          // [slot][H][DV][DK] or nullptr; may be final_state
+    float* final_state;
+    const int32_t *cu_seqlens, *slot_idx;
+    const uint8_t* has_init;
+    int64_t nslots, L, T;
     void* o;
     int H, share, DV, parts;
     float scale;
@@ -328,58 +377,99 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p)
                        __uint_as_float(w.y & 0xffff0000u));
 }
 
-template <typename T, int DK>
-__global__ void __launch_bounds__(kDecodeThreads) linear_decode_kernel(const LinearDecode p)
+// ONE: rows of exactly one token (decode).
+template <typename T, int DK, bool ONE>
+__global__ void __launch_bounds__(kShortThreads) linear_short_kernel(const LinearShort p)
 {
-    constexpr int kLanes = DK / 4, kRows = kDecodeThreads / kLanes;   // rows of one pass of the CTA
+    constexpr int kLanes = DK / 4, kRows = kShortThreads / kLanes;   // rows of one pass of the CTA
     const int64_t seq = blockIdx.y;
     const int h = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+    int64_t row = seq * p.L, n = p.L;
+    if (!ONE && p.cu_seqlens) {
+        row = p.cu_seqlens[seq];
+        row = row < 0 ? 0 : (row > p.T ? p.T : row);
+        const int64_t end = p.cu_seqlens[seq + 1];
+        n = (end < row ? row : (end > p.T ? p.T : end)) - row;
+        if (n > kLinearShort) return;                                // the scan's
+    }
     const int64_t slot = p.slot_idx ? (int64_t)p.slot_idx[seq] : seq;
     if (slot < 0 || slot >= p.nslots) return;
     const int l = threadIdx.x % kLanes, r0 = part * kRows * kRif + threadIdx.x / kLanes;
-    float4* S = reinterpret_cast<float4*>(p.state + ((slot * p.H + h) * p.DV) * DK) + l;
+    const int64_t at = ((slot * p.H + h) * p.DV) * DK + 4 * l;
+    const bool init = p.init && !(p.has_init && p.has_init[seq] == 0);
     float4 s[kRif];
 #pragma unroll
     for (int i = 0; i < kRif; ++i) {
         const int r = r0 + i * kRows;
-        if (r < p.DV) s[i] = S[(int64_t)r * kLanes];
+        s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (init && r < p.DV) s[i] = *reinterpret_cast<const float4*>(p.init + at + (int64_t)r * DK);
     }
     const LinearDecay decay(linear_log_decay(p.log_decay, h));
-    const float4 k = load4((const T*)p.k + seq * p.k_ld + (int64_t)(h / p.share) * DK + 4 * l);
-    const float4 q = load4((const T*)p.q + seq * p.q_ld + (int64_t)h * DK + 4 * l);
-    const T* vp = (const T*)p.v + seq * p.v_ld + (int64_t)(h / p.share) * p.DV;
-    T* op = (T*)p.o + seq * p.o_ld + (int64_t)h * p.DV;
+    const T* kp = (const T*)p.k + row * p.k_ld + (int64_t)(h / p.share) * DK + 4 * l;
+    const T* qp = (const T*)p.q + row * p.q_ld + (int64_t)h * DK + 4 * l;
+    const T* vp = (const T*)p.v + row * p.v_ld + (int64_t)(h / p.share) * p.DV;
+    T* op = (T*)p.o + row * p.o_ld + (int64_t)h * p.DV;
+    // a token's k, q and v are loaded while the one before is worked on
+    float4 k_next = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q_next = k_next;
+    float v_next[kRif];
+    auto fetch = [&]() {
+        k_next = load4(kp);
+        q_next = load4(qp);
 #pragma unroll
-    for (int i = 0; i < kRif; ++i) {
-        const int r = r0 + i * kRows;
-        const bool in = r < p.DV;
-        float o = 0.0f;
-        if (in) {
-            const float v = ld_f(vp + r);
-            float4 n;
-            n.x = decay.step(s[i].x, v * k.x);
-            n.y = decay.step(s[i].y, v * k.y);
-            n.z = decay.step(s[i].z, v * k.z);
-            n.w = decay.step(s[i].w, v * k.w);
-            S[(int64_t)r * kLanes] = n;
-            o = n.x * q.x + n.y * q.y + n.z * q.z + n.w * q.w;
+        for (int i = 0; i < kRif; ++i) v_next[i] = r0 + i * kRows < p.DV ? ld_f(vp + r0 + i * kRows) : 0.0f;
+        kp += p.k_ld;
+        qp += p.q_ld;
+        vp += p.v_ld;
+    };
+    if (ONE || n > 0) fetch();
+#pragma unroll 1
+    for (int64_t t = 0; t < (ONE ? 1 : n); ++t) {
+        const float4 k = k_next, q = q_next;
+        float vv[kRif];
+#pragma unroll
+        for (int i = 0; i < kRif; ++i) vv[i] = v_next[i];
+        if (!ONE && t + 1 < n) fetch();
+#pragma unroll
+        for (int i = 0; i < kRif; ++i) {
+            const int r = r0 + i * kRows;
+            const bool in = r < p.DV;
+            float o = 0.0f;
+            if (in) {
+                const float v = vv[i];
+                s[i].x = decay.step(s[i].x, v * k.x);
+                s[i].y = decay.step(s[i].y, v * k.y);
+                s[i].z = decay.step(s[i].z, v * k.z);
+                s[i].w = decay.step(s[i].w, v * k.w);
+                o = s[i].x * q.x + s[i].y * q.y + s[i].z * q.z + s[i].w * q.w;
+                if (ONE) *reinterpret_cast<float4*>(p.final_state + at + (int64_t)r * DK) = s[i];
+            }
+#pragma unroll
+            for (int off = kLanes / 2; off > 0; off >>= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
+            if (in && l == 0) op[r] = Act<T>::from_f(p.scale * o);
         }
+        op += p.o_ld;
+    }
+    if (!ONE) {
 #pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
-        if (in && l == 0) op[r] = Act<T>::from_f(p.scale * o);
+        for (int i = 0; i < kRif; ++i) {
+            const int r = r0 + i * kRows;
+            if (r < p.DV) *reinterpret_cast<float4*>(p.final_state + at + (int64_t)r * DK) = s[i];
+        }
     }
 }
 
-template <typename T>
-void launch_decode(const LinearDecode& p, int DK, int64_t b, cudaStream_t st)
+template <typename T, bool ONE>
+void launch_short(LinearShort p, int DK, int64_t b, cudaStream_t st)
 {
-    LaunchScope ls("linear_decode", st);
+    const int rows = kShortThreads / (DK / 4) * kRif;
+    p.parts = (p.DV + rows - 1) / rows;
+    LaunchScope ls(ONE ? "linear_decode" : "linear_short", st);
     const dim3 grid((unsigned)(p.H * p.parts), (unsigned)b);
     switch (DK) {
-    case 16: linear_decode_kernel<T, 16><<<grid, kDecodeThreads, 0, st>>>(p); break;
-    case 32: linear_decode_kernel<T, 32><<<grid, kDecodeThreads, 0, st>>>(p); break;
-    case 64: linear_decode_kernel<T, 64><<<grid, kDecodeThreads, 0, st>>>(p); break;
-    default: linear_decode_kernel<T, 128><<<grid, kDecodeThreads, 0, st>>>(p); break;
+    case 16: linear_short_kernel<T, 16, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
+    case 32: linear_short_kernel<T, 32, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
+    case 64: linear_short_kernel<T, 64, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
+    default: linear_short_kernel<T, 128, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
     }
 }
 
@@ -460,16 +550,27 @@ cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int6
     return cudaGetLastError();
 }
 
-cudaError_t launch_linear_decode(int64_t b, int H, int share, int DK, int DV, float scale, int act, const void* q,
-                                 int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
-                                 const float* log_decay, float* state, int64_t nslots, const int32_t* slot_idx, void* o,
-                                 int64_t o_ld, cudaStream_t st)
+cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st)
 {
-    LinearDecode p{q, k, v, q_ld, k_ld, v_ld, o_ld, log_decay, state, slot_idx, nslots, o, H, share, DV, 0, scale};
-    const int rows = kDecodeThreads / (DK / 4) * kRif;
-    p.parts = (DV + rows - 1) / rows;
-    if (act == SSD_BF16) launch_decode<__nv_bfloat16>(p, DK, b, st);
-    else launch_decode<float>(p, DK, b, st);
+    LaunchScope ls("linear_list", st);
+    linear_list_kernel<<<1, kListThreads, 0, st>>>(c);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, cudaStream_t st)
+{
+    LinearShort p{};
+    p.q = s.q; p.k = s.k; p.v = s.v; p.o = s.o;
+    p.q_ld = s.q_ld; p.k_ld = s.k_ld; p.v_ld = s.v_ld; p.o_ld = s.o_ld;
+    p.log_decay = c.log_decay;
+    p.init = s.init;
+    p.final_state = s.final_state;
+    p.cu_seqlens = c.cu_seqlens; p.slot_idx = c.slot_idx; p.has_init = c.has_init;
+    p.nslots = c.nslots; p.L = c.L; p.T = c.T;
+    p.H = c.H; p.share = s.k_share; p.DV = s.DV;
+    p.scale = s.out_scale;
+    if (c.act == SSD_BF16) one ? launch_short<__nv_bfloat16, true>(p, s.DK, c.b, st) : launch_short<__nv_bfloat16, false>(p, s.DK, c.b, st);
+    else one ? launch_short<float, true>(p, s.DK, c.b, st) : launch_short<float, false>(p, s.DK, c.b, st);
     return cudaGetLastError();
 }
 

@@ -46,14 +46,18 @@ struct LinearCall {
     // of a fixed-length one.
     int64_t seg_tokens, nseg, items;
     bool split;          // some row may have more than one segment
-    // 256 bytes at the start of the workspace: the status word, and (tensor cores, more segments than
-    // SMs) how many segments the CTAs of the states' and of the main pass have taken beyond their first.
-    // Those calls clear all of it beforehand; others leave the status word to the first kernel's block 0,
-    // as it starts: a block can only set it seconds later, when a wait gives up, or at its start for the
-    // reason that block 0 meets too.
+    // The first 256 bytes of the workspace: the status word, and (tensor cores) how many segments the CTAs
+    // have taken beyond their first, by launch. Where the counts are needed all of it is cleared
+    // beforehand; otherwise the first kernel's block 0 clears the status word as it starts: a block can
+    // only set it seconds later, when a wait gives up, or at its start for the reason that block 0 meets
+    // too.
     int* status;
     int* taken;
     bool clear_status;
+    // A packed call on the tensor cores works off lists of (sequence, segment), the longest first, made
+    // by launch_linear_list: `items` entries of the main pass, then of the states' pass, and their counts.
+    int2* list;
+    int* counts;
 };
 
 // Longest supported per-call counts keep every index in 32-bit grid dimensions.
@@ -65,10 +69,12 @@ cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStr
 cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st);
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,
                                     cudaStream_t st);
-cudaError_t launch_linear_decode(int64_t b, int H, int share, int DK, int DV, float scale, int act, const void* q,
-                                 int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
-                                 const float* log_decay, float* state, int64_t nslots, const int32_t* slot_idx, void* o,
-                                 int64_t o_ld, cudaStream_t st);
+// Forward scans of rows of at most kLinearShort tokens (one: of exactly one token each) on CUDA cores;
+// in a packed call, of those rows alone. A segment of the tensor-core scan costs an SM some 8 us however
+// short it is, 16 tokens of the recurrence 6.6 us.
+constexpr int kLinearShort = 8;
+cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st);
+cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, cudaStream_t st);
 // Segment length of a call's scans.
 int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms);
 
@@ -94,42 +100,48 @@ struct LinearItem {
     int64_t seq, slot, row0;
     int64_t n, seg, nseg;
 };
+// Segment `seg` of sequence `seq` of a packed call. The rows are clamped to the packed ones, so that no
+// cu_seqlens can reach outside them.
+__device__ __forceinline__ bool linear_packed_item(const LinearCall& c, int64_t seq, int64_t seg, LinearItem* it)
+{
+    int64_t start = c.cu_seqlens[seq], end = c.cu_seqlens[seq + 1];
+    it->slot = c.slot_idx ? (int64_t)c.slot_idx[seq] : seq;
+    start = start < 0 ? 0 : (start > c.T ? c.T : start);
+    end = end < start ? start : (end > c.T ? c.T : end);
+    const int64_t len = end - start;
+    it->seq = seq;
+    it->seg = seg;
+    it->nseg = len > 0 ? (len + c.seg_tokens - 1) / c.seg_tokens : 1;
+    it->row0 = start + seg * c.seg_tokens;
+    const int64_t left = len - seg * c.seg_tokens;
+    it->n = left < c.seg_tokens ? left : c.seg_tokens;
+    return seg >= 0 && seg < it->nseg && it->slot >= 0 && it->slot < c.nslots;
+}
+__device__ __forceinline__ int64_t linear_packed_first(const LinearCall& c, int64_t seq)   // item of its segment 0
+{
+    int64_t s = c.cu_seqlens[seq];
+    s = s < 0 ? 0 : (s > c.T ? c.T : s);
+    return seq + s / c.seg_tokens;
+}
 __device__ __forceinline__ bool linear_item(const LinearCall& c, int64_t item, LinearItem* it)
 {
-    int64_t start, len;
     if (c.cu_seqlens) {
-        // the largest i with i + floor(start_i / seg_tokens) <= item; the lengths are clamped to the
-        // packed rows, so that no cu_seqlens can reach outside them
+        // the largest i with i + floor(start_i / seg_tokens) <= item
         int64_t lo = 0, hi = c.b - 1;
         while (lo < hi) {
             const int64_t mid = (lo + hi + 1) >> 1;
-            int64_t s = c.cu_seqlens[mid];
-            s = s < 0 ? 0 : (s > c.T ? c.T : s);
-            if (mid + s / c.seg_tokens <= item) lo = mid;
+            if (linear_packed_first(c, mid) <= item) lo = mid;
             else hi = mid - 1;
         }
-        start = c.cu_seqlens[lo];
-        start = start < 0 ? 0 : (start > c.T ? c.T : start);
-        int64_t end = c.cu_seqlens[lo + 1];
-        end = end < start ? start : (end > c.T ? c.T : end);
-        len = end - start;
-        it->seq = lo;
-        it->seg = item - (lo + start / c.seg_tokens);
-        it->nseg = len > 0 ? (len + c.seg_tokens - 1) / c.seg_tokens : 1;
-        it->slot = c.slot_idx ? (int64_t)c.slot_idx[lo] : lo;
-        if (it->slot < 0 || it->slot >= c.nslots) return false;
-    } else {
-        it->seq = it->slot = item / c.nseg;
-        it->seg = item - it->seq * c.nseg;
-        it->nseg = c.nseg;
-        start = it->seq * c.L;
-        len = c.L;
+        return linear_packed_item(c, lo, item - linear_packed_first(c, lo), it);
     }
-    if (it->seg < 0 || it->seg >= it->nseg) return false;
-    it->row0 = start + it->seg * c.seg_tokens;
-    const int64_t left = len - it->seg * c.seg_tokens;
+    it->seq = it->slot = item / c.nseg;
+    it->seg = item - it->seq * c.nseg;
+    it->nseg = c.nseg;
+    it->row0 = it->seq * c.L + it->seg * c.seg_tokens;
+    const int64_t left = c.L - it->seg * c.seg_tokens;
     it->n = left < c.seg_tokens ? left : c.seg_tokens;
-    return true;
+    return it->seg < it->nseg;
 }
 // Whether the sequence continues from the state in its slot.
 __device__ __forceinline__ bool linear_has_init(const LinearCall& c, const LinearScan& s, int64_t seq)

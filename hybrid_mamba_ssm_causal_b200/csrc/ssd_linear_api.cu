@@ -47,7 +47,7 @@ bool row_ok(const void* p, int64_t ld, int64_t width, size_t es)
 }
 
 struct Layout {
-    size_t status, seg, part_k, part_v, total;   // seg: one region per scan
+    size_t status, list, seg, part_k, part_v, total;   // seg: one region per scan
     size_t seg_each;
 };
 
@@ -84,6 +84,8 @@ Layout layout(const ssd_linear_dims* d, const ssd::LinearCall& c, int nscans)
 {
     Layout w{};
     size_t off = 256;
+    w.list = off;
+    if (c.nseg == 0 && on_tensor_cores(d)) off = align256(off + (size_t)c.items * 2 * sizeof(int2));   // a packed call's segments
     w.seg = off;
     w.seg_each = c.split ? align256((size_t)c.items * d->nheads * d->dk * d->dv * 4) : 0;
     off += nscans * w.seg_each;
@@ -180,6 +182,10 @@ ssd_status ssd_mixer_linear_prefill(const ssd_linear_dims* d, const void* q, int
     c.taken = c.status + 1;
     c.clear_status = true;
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, init_state, o, o_ld, final_state, (char*)workspace, w);
+    if (d->seqlen <= ssd::kLinearShort) {
+        if (ssd::clear_device_status(c.status, st) != cudaSuccess) return SSD_ERR_CUDA;
+        return ssd::launch_linear_short(c, s, false, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    }
     return run(c, &s, 1, st);
 }
 
@@ -209,6 +215,10 @@ ssd_status ssd_mixer_linear_prefill_varlen(const ssd_linear_dims* d, const int32
     c.log_decay = log_decay;
     c.cu_seqlens = cu_seqlens;
     c.slot_idx = slot_idx;
+    if (on_tensor_cores(d)) {
+        c.list = (int2*)((char*)workspace + w.list);
+        c.counts = (int*)workspace + 32;
+    }
     c.has_init = has_init;
     c.nslots = nslots;
     c.status = (int*)workspace;
@@ -234,11 +244,13 @@ ssd_status ssd_mixer_linear_decode_step(const ssd_linear_dims* d, const void* q,
         !row_ok(q, q_ld, (int64_t)d->nheads * d->dk, es) || !row_ok(k, k_ld, (int64_t)d->ngroups * d->dk, es) ||
         !row_ok(v, v_ld, (int64_t)d->ngroups * d->dv, es) || !row_ok(o, o_ld, (int64_t)d->nheads * d->dv, es))
         return SSD_ERR_UNSUPPORTED;
-    return ssd::launch_linear_decode(d->batch, d->nheads, d->nheads / d->ngroups, d->dk, d->dv, d->scale, d->act, q, q_ld,
-                                     k, k_ld, v, v_ld, log_decay, state, nslots, slot_idx, o, o_ld,
-                                     (cudaStream_t)stream) == cudaSuccess
-               ? SSD_OK
-               : SSD_ERR_CUDA;
+    ssd::LinearCall c{};
+    c.b = d->batch; c.L = c.T = 1;
+    c.H = d->nheads; c.act = d->act;
+    c.log_decay = log_decay;
+    c.slot_idx = slot_idx; c.nslots = nslots;
+    const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, state, o, o_ld, state, nullptr, Layout{});
+    return ssd::launch_linear_short(c, s, true, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_mixer_linear_backward(const ssd_linear_dims* d, const void* q, int64_t q_ld, const void* k, int64_t k_ld,

@@ -215,6 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if (tid == 0) set_device_status(c.status, kDevSmemMisaligned);
         return;
     }
+    // segments of this launch, of every head and scan
+    const int64_t total = (c.list ? (int64_t)c.counts[STATES ? 1 : 0] : c.items) * c.H * a.nscans;
+    if ((int64_t)blockIdx.x >= total) return;
     Work* works = reinterpret_cast<Work*>(smem + C::kOffWork);
     static_assert(C::kOffBar >= C::kOffWork + 2 * sizeof(Work) && C::kOffBar % 8 == 0, "work slots");
     const uint32_t bar0 = sb + C::kOffBar;
@@ -581,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         // ------------------------------------------------------------------ one warp each
         regs_down<kRegsCtl>();
         if (warp == 16) {                                          // the list of segments, and their loads
-            const int64_t total = c.items * c.H * a.nscans;
             int64_t w = blockIdx.x;
             // The CTA's next segment: its first, then whichever no CTA has taken (lengths differ).
             auto next = [&]() {
@@ -596,14 +598,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             auto list = [&](int k) {
                 LinearItem it{};
                 int z = 0, h = 0;
+                int64_t item = 0;
                 bool rev = false;
                 for (;; w = next()) {
                     if (w >= total) break;
                     z = (int)(w % a.nscans);
                     h = (int)(w / a.nscans % c.H);
                     rev = a.s[z].reverse;
-                    if (!linear_item(c, w / a.nscans / c.H, &it)) continue;
-                    if (STATES && (rev ? it.seg == 0 : it.seg == it.nseg - 1)) continue;   // nothing follows it
+                    item = w / a.nscans / c.H;
+                    if (c.list) {
+                        const int2 e = c.list[(STATES ? c.items : 0) + item];
+                        linear_packed_item(c, e.x, e.y, &it);
+                        item = linear_packed_first(c, e.x) + e.y;
+                    } else {
+                        linear_item(c, item, &it);
+                        if (STATES && (rev ? it.seg == 0 : it.seg == it.nseg - 1)) continue;   // nothing follows it
+                    }
                     break;
                 }
                 const bool end = w >= total;
@@ -625,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         wk->scan = z;
                         wk->head = h;
                         wk->slot = (int)it.slot;
-                        wk->item = (int)(w / a.nscans / c.H);
+                        wk->item = (int)item;
                         wk->flags = (linear_has_init(c, a.s[z], it.seq) ? kFirstInit : 0) | (it.nseg > 1 ? kSplit : 0) |
                                     ((rev ? it.seg == 0 : it.seg == it.nseg - 1) ? kFinal : 0);
                     }
@@ -862,6 +872,11 @@ bool linear_tc_supported(const LinearScan& s, int act)
 cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st)
 {
     if (c.items == 0) return cudaSuccess;
+    if (c.cu_seqlens) {
+        cudaError_t e = launch_linear_list(c, st);
+        if (e == cudaSuccess) e = launch_linear_short(c, scans[0], false, st);
+        if (e != cudaSuccess) return e;
+    }
     const bool queue = c.items * c.H * nscans > device_sm_count();   // of any launch below
     bool done[kMaxScans] = {};
     for (int i = 0; i < nscans; ++i) {   // scans of one shape run in the same launches
@@ -870,10 +885,10 @@ cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int n
         TcMaps m;
         memset(&m, 0, sizeof(m));
         a.c = c;
-        a.c.clear_status = c.clear_status && !queue && i == 0;
-        if (queue) {
-            a.c.taken = c.taken + 2 * i;
-            const cudaError_t e = i > 0 ? cudaSuccess : cudaMemsetAsync(c.status, 0, 256, st);
+        a.c.clear_status = c.clear_status && !queue && i == 0 && !c.list;
+        a.c.taken = c.taken + 2 * i;
+        if (queue && i == 0 && !c.list) {
+            const cudaError_t e = cudaMemsetAsync(c.status, 0, 256, st);
             if (e != cudaSuccess) return e;
         }
         a.early = true;

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 SHAPES = [
     (1, 1, 1, 1, 64, 64), (2, 2, 3, 1, 64, 128), (1, 127, 2, 2, 128, 64), (1, 128, 4, 2, 128, 128),
     (3, 129, 2, 1, 64, 64), (2, 257, 5, 5, 128, 128), (1, 700, 3, 3, 64, 128), (1, 1100, 2, 1, 128, 128),
-    (2, 300, 300, 300, 64, 64),
+    (2, 300, 300, 300, 64, 64), (2, 7, 3, 3, 128, 64), (1, 8, 2, 1, 64, 64), (3, 9, 2, 2, 128, 128),
 ]
 SMALL = [(2, 37, 3, 3, 16, 32), (1, 200, 4, 2, 32, 16), (1, 65, 2, 2, 16, 16), (2, 190, 6, 2, 128, 32), (1, 333, 2, 1, 64, 16)]
 ALL = [(s, a) for s in SHAPES for a in ("bf16", "f32")] + [(s, a) for s in SMALL for a in ("bf16", "f32")]
@@ -91,11 +91,13 @@ def test_state_in_place_and_pieces(act, shape):
     check_forward(x, d, torch.cat(os, 1), st, d.scale)
 
 
-LENS = [[1], [0], [5, 0, 1, 130], [128, 256, 1, 127], [900, 3], [0, 0, 1000, 0], [64] * 20, [1] * 33]
+LENS = [[1], [0], [5, 0, 1, 130], [128, 256, 1, 127], [900, 3], [0, 0, 1000, 0], [64] * 20, [1] * 33, [7, 8, 9, 10, 0, 300, 8],
+        [1] * 40 + [2500, 2]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=lambda v: "-".join(map(str, v[:5])))
-@pytest.mark.parametrize("act,H,G,dk,dv", [("bf16", 4, 2, 64, 128), ("f32", 2, 2, 32, 16), ("bf16", 2, 1, 32, 32)])
+@pytest.mark.parametrize("act,H,G,dk,dv", [("bf16", 4, 2, 64, 128), ("f32", 2, 2, 32, 16), ("bf16", 2, 1, 32, 32),
+                                           ("bf16", 40, 40, 128, 128)])
 def test_packed(lens, act, H, G, dk, dv):
     """Packed sequences on slots: rows behind the last one, slots that no sequence owns and the other
     sequences' NaN stay out."""
