@@ -1,6 +1,8 @@
 // ssd_linear.cu -- linear attention with a decay per head on CUDA cores: the scan for any
 // supported shape and type, the state pass between segments, the sum over shared heads' gradients
 // and the decode step. The tensor-core scan is ssd_linear_tc.cu.
+#include <type_traits>
+
 #include "../../include/ssd_mixer.h"
 #include "ssd_common.cuh"
 #include "ssd_linear.h"
@@ -112,26 +114,19 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
         if (i + 1 < ntiles) fetch(i + 1);
         const int64_t t0 = (int64_t)tile_of(i) * kTile;
         const int nt = it.n - t0 < kTile ? (int)(it.n - t0) : kTile;
-        for (int x = 0; x < nt; ++x) {
-            const int tt = s.reverse ? nt - 1 - x : x;
+        // one token; `slow` is a constant of each of the two loops below, f its factor
+        const auto token = [&](int tt, auto slow_c, float f) {
+            constexpr bool slow = decltype(slow_c)::value;
             float kk[Sh::kCols], v[Sh::kRows];
 #pragma unroll
             for (int e = 0; e < Sh::kCols; ++e) kk[e] = ld_f(&s_in[tt][e0 + e]);
 #pragma unroll
             for (int r = 0; r < Sh::kRows; ++r) v[r] = s.u_scale * ld_f(&s_in[tt][2 * DK + d0 + r]);
-            if (fresh || decay.slow) {     // two versions, two operations an element each
-                const float f = fresh ? 0.0f : decay.f;
 #pragma unroll
-                for (int r = 0; r < Sh::kRows; ++r)
+            for (int r = 0; r < Sh::kRows; ++r)
 #pragma unroll
-                    for (int e = 0; e < Sh::kCols; ++e) S[r][e] = fmaf(f, S[r][e], fmaf(v[r], kk[e], S[r][e]));
-            } else {
-#pragma unroll
-                for (int r = 0; r < Sh::kRows; ++r)
-#pragma unroll
-                    for (int e = 0; e < Sh::kCols; ++e) S[r][e] = fmaf(decay.f, S[r][e], v[r] * kk[e]);
-            }
-            fresh = false;
+                for (int e = 0; e < Sh::kCols; ++e)
+                    S[r][e] = slow ? fmaf(f, S[r][e], fmaf(v[r], kk[e], S[r][e])) : fmaf(f, S[r][e], v[r] * kk[e]);
             if (!state_only) {
                 float o[Sh::kRows];
 #pragma unroll
@@ -159,7 +154,20 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
                 for (int off = Sh::kLanes / 16; off > 0; off >>= 1) o[0] += __shfl_xor_sync(0xffffffffu, o[0], off);
                 if ((l & (Sh::kLanes / 8 - 1)) == 0) s_o[tt][d0 + row] = s.out_scale * o[0];
             }
-        }
+        };
+        const auto walk = [&](auto slow_c) {
+            constexpr bool slow = decltype(slow_c)::value;
+            int x = 0;
+            if (fresh && nt > 0) {               // the first backward step has no decay
+                token(s.reverse ? nt - 1 : 0, slow_c, slow ? 0.0f : 1.0f);
+                fresh = false;
+                x = 1;
+            }
+#pragma unroll 4
+            for (; x < nt; ++x) token(s.reverse ? nt - 1 - x : x, slow_c, decay.f);
+        };
+        if (decay.slow) walk(std::true_type{});
+        else walk(std::false_type{});
         if (!state_only) {
             __syncthreads();
             for (int id = tid; id < nt * DV; id += kThr) {
@@ -504,13 +512,14 @@ cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStr
 
 // Splitting rows into segments fills SMs that whole rows would leave idle, at the price of a pass over
 // k and v before the main one and of the segments' states. Times in units of one block of 128 tokens
-// of the main pass. Tensor cores: a CTA per SM takes segment after segment, each some 0.8 to start; a
-// block of the states' pass is 0.5; the two more launches 2, and every segment's state goes through
-// memory four times. CUDA cores: two CTAs per SM or more, one segment each.
+// of the main pass. Tensor cores (some 3.3 us a block of 128 x 128): a CTA per SM takes segment after
+// segment, each some 1.8 to start and to end; a block of the states' pass is 0.5; the two more launches
+// 2, and every segment's state goes through memory four times. CUDA cores (token by token, some 20 us a
+// block): two CTAs per SM, one segment each; all the rest is small.
 int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms)
 {
     const int64_t rows = b * H * nscans, slots = tc ? sms : 2 * sms;
-    const double start = tc ? 0.8 : 1.5, states = tc ? 0.5 : 0.6, join = tc ? 2.0 : 3.0, each = tc ? 0.01 : 0.02;
+    const double start = tc ? 1.8 : 0.2, states = tc ? 0.5 : 0.6, join = tc ? 2.0 : 0.5, each = tc ? 0.01 : 0.003;
     const int64_t blocks = ((packed ? T : L) + 127) / 128;
     if (blocks <= 1 || b == 0) return 256;                 // nothing to split: longer than any row
     if (packed && b > 1) {

@@ -67,8 +67,9 @@ void plan(ssd::LinearCall* c, const ssd_linear_dims* d, bool packed, int nscans)
     c->L = d->seqlen;
     c->H = d->nheads;
     c->act = d->act;
-    c->seg_tokens = ssd::linear_segment_tokens(on_tensor_cores(d), d->batch, c->L, c->T, packed, d->nheads, nscans,
-                                               ssd::device_sm_count());
+    // on CUDA cores the scans of a backward pass run one after another
+    c->seg_tokens = ssd::linear_segment_tokens(on_tensor_cores(d), d->batch, c->L, c->T, packed, d->nheads,
+                                               on_tensor_cores(d) ? nscans : 1, ssd::device_sm_count());
     if (packed) {
         c->nseg = 0;
         c->items = d->batch > 0 ? d->batch + c->T / c->seg_tokens : 0;
