@@ -229,11 +229,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     auto v_free = [&](int i) { return bar0 + 144 + 8 * i; };
     auto w_full = [&](int i) { return bar0 + 160 + 8 * i; };
     auto w_empty = [&](int i) { return bar0 + 176 + 8 * i; };
+    // by stage, as the warp that waits may be more than a block behind
+    auto o_staged = [&](int i) { return bar0 + 264 + 8 * i; };
     const uint32_t qk_done = bar0 + 192, p_ready = bar0 + 200, inter_done = bar0 + 208, inter_read = bar0 + 216,
-                   intra_done = bar0 + 224, o_free = bar0 + 232, o_staged = bar0 + 240, u_done = bar0 + 248,
-                   u_free = bar0 + 256, s_ready = bar0 + 264;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 272);
-    static_assert(C::kOffBar + 276 <= C::kSmem, "barriers");
+                   intra_done = bar0 + 224, o_free = bar0 + 232, u_done = bar0 + 240, u_free = bar0 + 248,
+                   s_ready = bar0 + 256;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 296);
+    static_assert(C::kOffBar + 300 <= C::kSmem, "barriers");
     constexpr int kReaders = STATES ? 13 : 19;   // warps that read a work slot
 
     if (tid == 0) {
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
             mbar_init(kv_full(i), 1);
+            mbar_init(o_staged(i), 128);
             mbar_init(kv_empty(i), STATES ? 1 : 2);   // U's MMAs, and intra's or the stores
         }
         for (int i = 0; i < 2; ++i) {
@@ -255,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         mbar_init(inter_read, 128);
         mbar_init(intra_done, 1);
         mbar_init(o_free, 128);
-        mbar_init(o_staged, 128);
         mbar_init(u_done, 1);
         mbar_init(u_free, 128);
         mbar_init(s_ready, 128);
@@ -267,7 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     bool ok = true;
-    auto wait = [&](uint32_t bar, int n) {   // the barrier's n-th completion (from 0)
+    // The barrier's n-th completion (from 0). A wait tells a completion from the one before it only, so
+    // nobody may be two ahead of a wait for it: each barrier's next but one completion needs an arrival
+    // that comes after the wait.
+    auto wait = [&](uint32_t bar, int n) {
         if (ok && !mbar_wait_bounded(bar, (uint32_t)(n & 1), kWait)) ok = false;
     };
     // The k-th segment of this CTA; nullptr: there are no more, or a wait gave up, in which case all
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         }
                     }
                     fence_async_smem();
-                    mbar_arrive_local(o_staged);
+                    mbar_arrive_local(o_staged(st));
                 }
                 close(k);
             }
@@ -743,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     const int per = s.o_f32 ? 32 : 64, nb = (wk->n + kB - 1) / kB, c0 = wk->head * DV;
                     for (int x0 = 0; x0 < nb; ++x0, ++i) {
                         const int st = i % C::kStages, b = block(s.reverse, nb, x0);
-                        wait(o_staged, i);
+                        wait(o_staged(st), i / C::kStages);
                         if (tokens(wk->n, b) == kB) {
                             for (int x = 0; x < DV / per; ++x)
                                 tma_store_3d(m, sb + (uint32_t)st * C::kStage + x * kAtom, c0 + per * x, wk->row0 + b * kB, 0);

@@ -219,6 +219,35 @@ def check_backward(x, d, g):
     check("dinit_state", g["init_state"], ref["init_state"], mag["init_state"], d, L, state=True)
 
 
+@pytest.mark.parametrize("act,dk,dv", [("bf16", 64, 128), ("f32", 16, 32)])
+def test_backward_of_no_tokens(act, dk, dv):
+    d = dims(2, 0, 3, 3, dk, dv, act)
+    x = make(2, 0, 3, 3, dk, dv, act, seed=1)
+    g = sm.linear_backward(d, x["q"], x["k"], x["v"], x["log_decay"], x["do"], x["init"], x["dfinal"])
+    assert torch.equal(g["init_state"], x["dfinal"]) and g["q"].shape == (2, 0, 3 * dk)
+
+
+@pytest.mark.parametrize("shape", [(1, 16384, 5, 5, 64, 64), (1, 6000, 2, 1, 128, 128), (5, 1290, 64, 64, 64, 64)])
+def test_long_and_many_rows(shape):
+    """Rows of many blocks, cut and whole, and more segments than SMs, forwards and backwards. The fp64
+    form runs head by head; the bound is that of the sizes."""
+    b, L, H, G, dk, dv = shape
+    d = dims(*shape, "bf16")
+    x = make(*shape, "bf16", seed=L)
+    o, fs = forward(x, d)
+    g = sm.linear_backward(d, x["q"], x["k"], x["v"], x["log_decay"], x["do"], x["init"], x["dfinal"]) if G == H else None
+    one = dims(1, L, 1, 1, dk, dv, "bf16")
+    for i, h in {(0, 0), (b - 1, H - 1), (b // 2, H // 2)}:
+        r = H // G
+        y = {"q": x["q"].view(b, L, H, dk)[i:i + 1, :, h], "do": x["do"].view(b, L, H, dv)[i:i + 1, :, h],
+             "k": x["k"].view(b, L, G, dk)[i:i + 1, :, h // r], "v": x["v"].view(b, L, G, dv)[i:i + 1, :, h // r],
+             "log_decay": x["log_decay"][h:h + 1], "init": x["init"][i:i + 1, h:h + 1], "dfinal": x["dfinal"][i:i + 1, h:h + 1]}
+        check_forward(y, one, o.view(b, L, H, dv)[i:i + 1, :, h], fs[i:i + 1, h:h + 1], d.scale)
+        if g is not None and L <= 6000:
+            check_backward(y, one, {"q": g["q"].view(b, L, H, dk)[i:i + 1, :, h], "k": g["k"].view(b, L, G, dk)[i:i + 1, :, h],
+                                    "v": g["v"].view(b, L, G, dv)[i:i + 1, :, h], "init_state": g["init_state"][i:i + 1, h:h + 1]})
+
+
 @pytest.mark.parametrize("decay", [[0.0], [-math.inf], [-200.0, -1e-5]])
 @pytest.mark.parametrize("act,shape", [("bf16", (1, 290, 2, 2, 128, 64)), ("f32", (1, 100, 2, 1, 16, 32))])
 def test_backward_extreme_decays(decay, act, shape):
