@@ -224,10 +224,10 @@ void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, cudaStrea
 }
 
 // ------------------------------------------------------------- states between segments
-// Rows of one segment are left alone. Before: seg_states[t] holds segment t's own state from a zero
-// start (the last segment of the scan has none). After: the state entering segment t. A block takes
-// 4096 elements of one (sequence, head); a thread's loads of the next segment are under way while one
-// is added.
+// Rows of one segment are left alone. Before: seg_states[t] holds piece t's own state from a zero start
+// (the pieces of the scan's last segment have none). After: at each segment's first piece in scan order,
+// the state entering it. A block takes 4096 elements of one (sequence, head); a thread's loads of the
+// next piece are under way while one is added.
 constexpr int kPassElems = 4096;
 __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, const LinearScan s)
 {
@@ -244,11 +244,13 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
     }
     __syncthreads();
     const int64_t nseg = first.nseg;
-    if (nseg < 2) return;
+    // pieces before the scan's last segment, whose entering state ends the walk
+    const int64_t before = s.reverse ? nseg - c.sub : (nseg - 1) / c.sub * c.sub;
+    if (before < 1) return;
     const float g = linear_log_decay(c.log_decay, h);
     const bool init = linear_has_init(c, s, seq);
     const float* ip = s.init ? s.init + (first.slot * c.H + h) * (int64_t)hs : nullptr;
-    // segments in scan order; the short one is the row's last
+    // pieces in scan order; the short one is the row's last
     auto at = [&](int64_t k) { return s.seg_states + ((item0 + (s.reverse ? nseg - 1 - k : k)) * c.H + h) * (int64_t)hs; };
     constexpr int kV = kPassElems / 1024;
     float4 S[kV], own[kV];
@@ -264,18 +266,19 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
         }
     }
     const LinearDecay whole(g * (float)c.seg_tokens);
-    for (int64_t k = 0; k < nseg; ++k) {
+    for (int64_t k = 0; k <= before; ++k) {
         float4 next[kV];
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             next[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (e0 + v * 1024 < hs && k + 2 < nseg) next[v] = *reinterpret_cast<const float4*>(at(k + 1) + e0 + v * 1024);
+            if (e0 + v * 1024 < hs && k + 1 < before) next[v] = *reinterpret_cast<const float4*>(at(k + 1) + e0 + v * 1024);
         }
-        // backwards the short segment comes first (only fixed-length rows run backwards)
+        const bool starts = s.reverse ? k == 0 || (nseg - 1 - k) % c.sub == c.sub - 1 : k % c.sub == 0;
+        // backwards the short piece comes first (only fixed-length rows run backwards)
         const LinearDecay d = s.reverse && k == 0 ? LinearDecay(g * (float)(c.L - (nseg - 1) * c.seg_tokens)) : whole;
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            if (e0 + v * 1024 < hs) *reinterpret_cast<float4*>(at(k) + e0 + v * 1024) = S[v];
+            if (starts && e0 + v * 1024 < hs) *reinterpret_cast<float4*>(at(k) + e0 + v * 1024) = S[v];
             S[v] = make_float4(d.step(S[v].x, own[v].x), d.step(S[v].y, own[v].y), d.step(S[v].z, own[v].z), d.step(S[v].w, own[v].w));
             own[v] = next[v];
         }
@@ -497,7 +500,7 @@ cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStr
     if (c.split) {
         cudaError_t e = run(true);
         if (e != cudaSuccess) return e;
-        e = launch_linear_pass(c, s, st);
+        e = launch_linear_pass(linear_pieces(c), s, st);
         if (e != cudaSuccess) return e;
     }
     return run(false);
@@ -516,11 +519,12 @@ cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStr
 // segment, each some 1.8 to start and to end; a block of the states' pass is 0.5; the two more launches
 // 2, and every segment's state goes through memory four times. CUDA cores (token by token, some 20 us a
 // block): two CTAs per SM, one segment each; all the rest is small.
-int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms)
+int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms, int* sub)
 {
     const int64_t rows = b * H * nscans, slots = tc ? sms : 2 * sms;
-    const double start = tc ? 1.8 : 0.2, states = tc ? 0.5 : 0.6, join = tc ? 2.0 : 0.5, each = tc ? 0.01 : 0.003;
+    const double start = tc ? 1.8 : 0.2, states = tc ? 0.58 : 0.6, join = tc ? 2.0 : 0.5, each = tc ? 0.01 : 0.003;
     const int64_t blocks = ((packed ? T : L) + 127) / 128;
+    *sub = 1;
     if (blocks <= 1 || b == 0) return 256;                 // nothing to split: longer than any row
     if (packed && b > 1) {
         // The lengths are not known here. Segments are twice an SM's even share of all blocks (and 8 at
@@ -529,22 +533,24 @@ int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool pac
         const int64_t share = (blocks * H * nscans + slots - 1) / slots;
         return (2 * share > 8 ? 2 * share : 8) * 128;
     }
-    const int64_t per_row = blocks;
-    double best = 0.0;
-    int64_t best_seg = 0;
-    for (int64_t nseg = 1; nseg <= per_row && nseg <= 256; ++nseg) {
-        const int64_t seg = (per_row + nseg - 1) / nseg;
-        if (best_seg && seg == best_seg) continue;
-        const int64_t n = rows * ((per_row + seg - 1) / seg);
-        double cost = (double)((n + slots - 1) / slots) * (seg + start);
-        if (seg < per_row)
-            cost += (double)((n - rows + slots - 1) / slots) * (states * seg + start) + join + each * (double)n * 148.0 / (double)sms;
-        if (!best_seg || cost < best) {
-            best = cost;
-            best_seg = seg;
+    const auto rounds = [&](int64_t n) { return (double)((n + slots - 1) / slots); };
+    double best = rounds(rows) * ((double)blocks + start);   // whole rows
+    int64_t best_seg = blocks + 1;
+    for (int64_t nseg = 2; nseg <= blocks && nseg <= 256; ++nseg) {
+        for (int m = 1; m <= (tc && !packed ? 4 : 1); ++m) {
+            const int64_t piece = (blocks + nseg * m - 1) / (nseg * m), seg = piece * m;
+            const int64_t n = rows * ((blocks + seg - 1) / seg), pieces = (n - rows) * m;
+            if (n == rows) continue;
+            const double cost = rounds(n) * ((double)seg + start) + rounds(pieces) * (states * (double)piece + start) + join +
+                                each * (double)pieces * 148.0 / (double)sms;
+            if (cost < best) {
+                best = cost;
+                best_seg = seg;
+                *sub = m;
+            }
         }
     }
-    return (best_seg >= per_row ? blocks + 1 : best_seg) * 128;
+    return best_seg * 128;
 }
 
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,

@@ -46,6 +46,10 @@ struct LinearCall {
     // of a fixed-length one.
     int64_t seg_tokens, nseg, items;
     bool split;          // some row may have more than one segment
+    // The states' pass of fixed-length rows works on pieces of seg_tokens / sub tokens, to fill SMs that
+    // few segments would leave idle: linear_pieces(c) is the call that it sees, and seg_states is laid
+    // out by those pieces.
+    int sub;
     // The first 256 bytes of the workspace: the status word, and (tensor cores) how many segments the CTAs
     // have taken beyond their first, by launch. Where the counts are needed all of it is cleared
     // beforehand; otherwise the first kernel's block 0 clears the status word as it starts: a block can
@@ -60,12 +64,24 @@ struct LinearCall {
     int* counts;
 };
 
+inline LinearCall linear_pieces(const LinearCall& c)
+{
+    LinearCall f = c;
+    if (c.sub > 1) {
+        f.seg_tokens = c.seg_tokens / c.sub;
+        f.nseg = (c.L + f.seg_tokens - 1) / f.seg_tokens;
+        f.items = c.b * f.nseg;
+    }
+    return f;
+}
+
 // Longest supported per-call counts keep every index in 32-bit grid dimensions.
 bool linear_tc_supported(const LinearScan& s, int act);
 // nscans scans (1, or the 3 of a backward pass) in as few launches as the split allows.
 cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st);
 cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStream_t st);
-// The states entering every segment of rows that have more than one, from the segments' own states.
+// The states entering every segment of rows that have more than one, from the pieces' own states; c as
+// linear_pieces gives it.
 cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st);
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,
                                     cudaStream_t st);
@@ -75,8 +91,8 @@ cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int6
 constexpr int kLinearShort = 8;
 cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st);
 cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, cudaStream_t st);
-// Segment length of a call's scans.
-int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms);
+// Segment length of a call's scans, and the pieces of a segment in the states' pass.
+int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms, int* sub);
 
 #ifdef __CUDACC__
 

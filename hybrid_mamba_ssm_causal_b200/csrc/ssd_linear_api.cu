@@ -69,7 +69,7 @@ void plan(ssd::LinearCall* c, const ssd_linear_dims* d, bool packed, int nscans)
     c->act = d->act;
     // on CUDA cores the scans of a backward pass run one after another
     c->seg_tokens = ssd::linear_segment_tokens(on_tensor_cores(d), d->batch, c->L, c->T, packed, d->nheads,
-                                               on_tensor_cores(d) ? nscans : 1, ssd::device_sm_count());
+                                               on_tensor_cores(d) ? nscans : 1, ssd::device_sm_count(), &c->sub);
     if (packed) {
         c->nseg = 0;
         c->items = d->batch > 0 ? d->batch + c->T / c->seg_tokens : 0;
@@ -88,7 +88,7 @@ Layout layout(const ssd_linear_dims* d, const ssd::LinearCall& c, int nscans)
     w.list = off;
     if (c.nseg == 0 && on_tensor_cores(d)) off = align256(off + (size_t)c.items * 2 * sizeof(int2));   // a packed call's segments
     w.seg = off;
-    w.seg_each = c.split ? align256((size_t)c.items * d->nheads * d->dk * d->dv * 4) : 0;
+    w.seg_each = c.split ? align256((size_t)ssd::linear_pieces(c).items * d->nheads * d->dk * d->dv * 4) : 0;
     off += nscans * w.seg_each;
     w.part_k = off;
     if (nscans == 3 && d->nheads != d->ngroups) off = align256(off + (size_t)c.T * d->nheads * d->dk * 4);

@@ -617,7 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         item = linear_packed_first(c, e.x) + e.y;
                     } else {
                         linear_item(c, item, &it);
-                        if (STATES && (rev ? it.seg == 0 : it.seg == it.nseg - 1)) continue;   // nothing follows it
+                        // pieces of the scan's last segment: nothing follows it
+                        if (STATES && (rev ? it.seg < c.sub : it.seg / c.sub == (it.nseg - 1) / c.sub)) continue;
+                        if (!STATES && c.sub > 1) {        // the first in scan order of the segment's pieces
+                            const int64_t piece = c.seg_tokens / c.sub, pieces = (c.L + piece - 1) / piece;
+                            const int64_t p = it.seg * c.sub + (rev ? c.sub - 1 : 0);
+                            item = it.seq * pieces + (p < pieces ? p : pieces - 1);
+                        }
                     }
                     break;
                 }
@@ -857,8 +863,10 @@ template <int DK, int DV>
 cudaError_t launch_shape(const TcArgs& a, const TcMaps& m, cudaStream_t st)
 {
     if (a.c.split) {
-        cudaError_t e = launch_one<DK, DV, true>(a, m, st);
-        for (int i = 0; i < a.nscans && e == cudaSuccess; ++i) e = launch_linear_pass(a.c, a.s[i], st);
+        TcArgs fine = a;
+        fine.c = linear_pieces(a.c);
+        cudaError_t e = launch_one<DK, DV, true>(fine, m, st);
+        for (int i = 0; i < a.nscans && e == cudaSuccess; ++i) e = launch_linear_pass(fine.c, a.s[i], st);
         if (e != cudaSuccess) return e;
         TcArgs after = a;
         after.c.clear_status = false;
@@ -882,7 +890,7 @@ cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int n
         if (e == cudaSuccess) e = launch_linear_short(c, scans[0], false, st);
         if (e != cudaSuccess) return e;
     }
-    const bool queue = c.items * c.H * nscans > device_sm_count();   // of any launch below
+    const bool queue = linear_pieces(c).items * c.H * nscans > device_sm_count();   // of any launch below
     bool done[kMaxScans] = {};
     for (int i = 0; i < nscans; ++i) {   // scans of one shape run in the same launches
         if (done[i]) continue;
