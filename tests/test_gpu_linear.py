@@ -227,7 +227,8 @@ def test_backward_of_no_tokens(act, dk, dv):
     assert torch.equal(g["init_state"], x["dfinal"]) and g["q"].shape == (2, 0, 3 * dk)
 
 
-@pytest.mark.parametrize("shape", [(1, 16384, 5, 5, 64, 64), (1, 6000, 2, 1, 128, 128), (5, 1290, 64, 64, 64, 64)])
+@pytest.mark.parametrize("shape", [(1, 16384, 5, 5, 64, 64), (1, 6000, 2, 1, 128, 128), (5, 1290, 64, 64, 64, 64),
+                                   (1, 2500, 20, 20, 128, 64), (1, 5001, 60, 60, 64, 64)])
 def test_long_and_many_rows(shape):
     """Rows of many blocks, cut and whole, and more segments than SMs, forwards and backwards. The fp64
     form runs head by head; the bound is that of the sizes."""
