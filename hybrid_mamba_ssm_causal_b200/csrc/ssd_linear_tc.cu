@@ -641,14 +641,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 #pragma unroll 1
                     for (int e = lane; e < 256; e += 32) wk->pow[e] = power(abs(e - 127));
                     if (lane == 0) {
+                        const bool init = linear_has_init(c, a.s[z], it.seq), split = it.nseg > 1;
                         wk->log_l = g;
                         wk->row0 = (int)it.row0;
                         wk->scan = z;
                         wk->head = h;
                         wk->slot = (int)it.slot;
                         wk->item = (int)item;
-                        wk->flags = (linear_has_init(c, a.s[z], it.seq) ? kFirstInit : 0) | (it.nseg > 1 ? kSplit : 0) |
+                        wk->flags = (init ? kFirstInit : 0) | (split ? kSplit : 0) |
                                     ((rev ? it.seg == 0 : it.seg == it.nseg - 1) ? kFinal : 0);
+                        if (!STATES && (init || split)) {      // the state that enters, on its way to L2 by the time it is wanted
+                            const float* p = split ? a.s[z].seg_states + (item * c.H + h) * (int64_t)(DK * DV)
+                                                   : a.s[z].init + (it.slot * c.H + h) * (int64_t)(DK * DV);
+                            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(DK * DV * 4) : "memory");
+                        }
                     }
                 }
                 if (lane == 0) wk->n = end ? -1 : (int)it.n;
