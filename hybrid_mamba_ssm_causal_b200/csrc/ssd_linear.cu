@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     constexpr int kPer = (kTileVecs + kThr - 1) / kThr;
     __shared__ __align__(16) T s_in[kTile][2 * DK + DV];      // k, then q, then v
     __shared__ __align__(16) float s_o[kTile][DV];
+    linear_follow();
     if (c.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *c.status = kDevOk;
 
     const int h = blockIdx.x % c.H;
@@ -196,30 +197,30 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
 }
 
 template <typename T, int DK, int DV>
-void launch_scan_shape(const LinearCall& c, const LinearScan& s, bool state_only, cudaStream_t st)
+void launch_scan_shape(const LinearCall& c, const LinearScan& s, bool state_only, bool follows, cudaStream_t st)
 {
     constexpr int kWarps = DV / SimtShape<DK>::kWarpRows > 0 ? DV / SimtShape<DK>::kWarpRows : 1;
     LaunchScope ls(state_only ? "linear_states" : "linear_scan", st);
-    linear_scan_kernel<T, DK, DV><<<(unsigned)(c.items * c.H), 32 * kWarps, 0, st>>>(c, s, state_only);
+    linear_launch(follows, linear_scan_kernel<T, DK, DV>, dim3((unsigned)(c.items * c.H)), 32 * kWarps, 0, st, c, s, state_only);
 }
 template <typename T, int DK>
-void launch_scan_dv(const LinearCall& c, const LinearScan& s, bool so, cudaStream_t st)
+void launch_scan_dv(const LinearCall& c, const LinearScan& s, bool so, bool follows, cudaStream_t st)
 {
     switch (s.DV) {
-    case 16: return launch_scan_shape<T, DK, 16>(c, s, so, st);
-    case 32: return launch_scan_shape<T, DK, 32>(c, s, so, st);
-    case 64: return launch_scan_shape<T, DK, 64>(c, s, so, st);
-    default: return launch_scan_shape<T, DK, 128>(c, s, so, st);
+    case 16: return launch_scan_shape<T, DK, 16>(c, s, so, follows, st);
+    case 32: return launch_scan_shape<T, DK, 32>(c, s, so, follows, st);
+    case 64: return launch_scan_shape<T, DK, 64>(c, s, so, follows, st);
+    default: return launch_scan_shape<T, DK, 128>(c, s, so, follows, st);
     }
 }
 template <typename T>
-void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, cudaStream_t st)
+void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, bool follows, cudaStream_t st)
 {
     switch (s.DK) {
-    case 16: return launch_scan_dv<T, 16>(c, s, so, st);
-    case 32: return launch_scan_dv<T, 32>(c, s, so, st);
-    case 64: return launch_scan_dv<T, 64>(c, s, so, st);
-    default: return launch_scan_dv<T, 128>(c, s, so, st);
+    case 16: return launch_scan_dv<T, 16>(c, s, so, follows, st);
+    case 32: return launch_scan_dv<T, 32>(c, s, so, follows, st);
+    case 64: return launch_scan_dv<T, 64>(c, s, so, follows, st);
+    default: return launch_scan_dv<T, 128>(c, s, so, follows, st);
     }
 }
 
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
     const int h = blockIdx.y;
     const int64_t seq = blockIdx.z;
     const int hs = s.DK * s.DV, e0 = blockIdx.x * kPassElems + 4 * threadIdx.x;
+    linear_follow();
     if (c.cu_seqlens && (int64_t)c.cu_seqlens[seq + 1] - c.cu_seqlens[seq] <= c.seg_tokens) return;
     if (threadIdx.x == 0) {
         item0 = c.cu_seqlens ? linear_packed_first(c, seq) : seq * c.nseg;
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(256) linear_group_sum_kernel(const float* __re
                                                                int64_t n, int G, int r, int D)
 {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    linear_follow();
     if (i >= n) return;
     const int64_t w = (int64_t)G * D, row = i / w;
     const int col = (int)(i - row * w), g = col / D, d = col - g * D;
@@ -313,6 +316,7 @@ constexpr int kListThreads = 1024, kBuckets = 256;
 __global__ void __launch_bounds__(kListThreads) linear_list_kernel(const LinearCall c)
 {
     __shared__ int start[2][kBuckets];
+    linear_follow();
     if (threadIdx.x < 64) c.status[threadIdx.x] = 0;          // the status word, the counts, what is taken
     for (int i = threadIdx.x; i < 2 * kBuckets; i += kListThreads) (&start[0][0])[i] = 0;
     __syncthreads();
@@ -395,6 +399,7 @@ __global__ void __launch_bounds__(kShortThreads) linear_short_kernel(const Linea
     constexpr int kLanes = DK / 4, kRows = kShortThreads / kLanes;   // rows of one pass of the CTA
     const int64_t seq = blockIdx.y;
     const int h = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+    if (!ONE) linear_follow();
     int64_t row = seq * p.L, n = p.L;
     if (!ONE && p.cu_seqlens) {
         row = p.cu_seqlens[seq];
@@ -470,47 +475,43 @@ __global__ void __launch_bounds__(kShortThreads) linear_short_kernel(const Linea
 }
 
 template <typename T, bool ONE>
-void launch_short(LinearShort p, int DK, int64_t b, cudaStream_t st)
+cudaError_t launch_short(LinearShort p, int DK, int64_t b, bool follows, cudaStream_t st)
 {
     const int rows = kShortThreads / (DK / 4) * kRif;
     p.parts = (p.DV + rows - 1) / rows;
     LaunchScope ls(ONE ? "linear_decode" : "linear_short", st);
     const dim3 grid((unsigned)(p.H * p.parts), (unsigned)b);
     switch (DK) {
-    case 16: linear_short_kernel<T, 16, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
-    case 32: linear_short_kernel<T, 32, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
-    case 64: linear_short_kernel<T, 64, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
-    default: linear_short_kernel<T, 128, ONE><<<grid, kShortThreads, 0, st>>>(p); break;
+    case 16: return linear_launch(follows, linear_short_kernel<T, 16, ONE>, grid, kShortThreads, 0, st, p);
+    case 32: return linear_launch(follows, linear_short_kernel<T, 32, ONE>, grid, kShortThreads, 0, st, p);
+    case 64: return linear_launch(follows, linear_short_kernel<T, 64, ONE>, grid, kShortThreads, 0, st, p);
+    default: return linear_launch(follows, linear_short_kernel<T, 128, ONE>, grid, kShortThreads, 0, st, p);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStream_t st)
+cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, bool follows, cudaStream_t st)
 {
     if (c.items == 0) return cudaSuccess;
-    LinearCall call = c;
-    const auto run = [&](bool state_only) {
-        const LinearCall c = call;
-        call.clear_status = false;
-        if (c.act == SSD_BF16) launch_scan_dk<__nv_bfloat16>(c, s, state_only, st);
-        else launch_scan_dk<float>(c, s, state_only, st);
+    const auto run = [&](const LinearCall& call, bool state_only, bool after) {
+        if (c.act == SSD_BF16) launch_scan_dk<__nv_bfloat16>(call, s, state_only, after, st);
+        else launch_scan_dk<float>(call, s, state_only, after, st);
         return cudaGetLastError();
     };
-    if (c.split) {
-        cudaError_t e = run(true);
-        if (e != cudaSuccess) return e;
-        e = launch_linear_pass(linear_pieces(c), s, st);
-        if (e != cudaSuccess) return e;
-    }
-    return run(false);
+    if (!c.split) return run(c, false, follows);
+    cudaError_t e = run(c, true, follows);
+    if (e == cudaSuccess) e = launch_linear_pass(c, s, st);
+    LinearCall after = c;
+    after.clear_status = false;
+    return e == cudaSuccess ? run(after, false, true) : e;
 }
 
 cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st)
 {
     LaunchScope ls("linear_pass", st);
-    linear_pass_kernel<<<dim3((unsigned)((s.DK * s.DV + kPassElems - 1) / kPassElems), (unsigned)c.H, (unsigned)c.b), 256, 0, st>>>(c, s);
-    return cudaGetLastError();
+    return linear_launch(true, linear_pass_kernel, dim3((unsigned)((s.DK * s.DV + kPassElems - 1) / kPassElems), (unsigned)c.H, (unsigned)c.b),
+                         256, 0, st, c, s);
 }
 
 // Splitting rows into segments fills SMs that whole rows would leave idle, at the price of a pass over
@@ -560,9 +561,8 @@ cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int6
     if (n == 0) return cudaSuccess;
     LaunchScope ls("linear_group_sum", st);
     const unsigned grid = (unsigned)((n / 4 + 255) / 256);
-    if (act == SSD_BF16) linear_group_sum_kernel<<<grid, 256, 0, st>>>(in, (__nv_bfloat16*)out, ld, n, G, r, D);
-    else linear_group_sum_kernel<<<grid, 256, 0, st>>>(in, (float*)out, ld, n, G, r, D);
-    return cudaGetLastError();
+    return act == SSD_BF16 ? linear_launch(true, linear_group_sum_kernel<__nv_bfloat16>, dim3(grid), 256, 0, st, in, (__nv_bfloat16*)out, ld, n, G, r, D)
+                           : linear_launch(true, linear_group_sum_kernel<float>, dim3(grid), 256, 0, st, in, (float*)out, ld, n, G, r, D);
 }
 
 cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st)
@@ -572,7 +572,7 @@ cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st)
     return cudaGetLastError();
 }
 
-cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, cudaStream_t st)
+cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, bool follows, cudaStream_t st)
 {
     LinearShort p{};
     p.q = s.q; p.k = s.k; p.v = s.v; p.o = s.o;
@@ -584,9 +584,9 @@ cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool o
     p.nslots = c.nslots; p.L = c.L; p.T = c.T;
     p.H = c.H; p.share = s.k_share; p.DV = s.DV;
     p.scale = s.out_scale;
-    if (c.act == SSD_BF16) one ? launch_short<__nv_bfloat16, true>(p, s.DK, c.b, st) : launch_short<__nv_bfloat16, false>(p, s.DK, c.b, st);
-    else one ? launch_short<float, true>(p, s.DK, c.b, st) : launch_short<float, false>(p, s.DK, c.b, st);
-    return cudaGetLastError();
+    if (c.act == SSD_BF16)
+        return one ? launch_short<__nv_bfloat16, true>(p, s.DK, c.b, follows, st) : launch_short<__nv_bfloat16, false>(p, s.DK, c.b, follows, st);
+    return one ? launch_short<float, true>(p, s.DK, c.b, follows, st) : launch_short<float, false>(p, s.DK, c.b, follows, st);
 }
 
 }  // namespace ssd

@@ -79,10 +79,11 @@ inline LinearCall linear_pieces(const LinearCall& c)
 bool linear_tc_supported(const LinearScan& s, int act);
 // nscans scans (1, or the 3 of a backward pass) in as few launches as the split allows.
 cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st);
-cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, cudaStream_t st);
+cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, bool follows, cudaStream_t st);
 // The states entering every segment of rows that have more than one, from the pieces' own states; c as
 // linear_pieces gives it.
-cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st);
+cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st);   // follows a launch
+// (follows a launch)
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,
                                     cudaStream_t st);
 // Forward scans of rows of at most kLinearShort tokens (one: of exactly one token each) on CUDA cores;
@@ -90,11 +91,37 @@ cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int6
 // short it is, 16 tokens of the recurrence 6.6 us.
 constexpr int kLinearShort = 8;
 cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st);
-cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, cudaStream_t st);
+// `follows`: it comes after another kernel of the call.
+cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, bool follows, cudaStream_t st);
 // Segment length of a call's scans, and the pieces of a segment in the states' pass.
 int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms, int* sub);
 
 #ifdef __CUDACC__
+
+// A call's kernels follow one another by programmatic dependent launch: each lets its successor start
+// (blocks placed, shared and tensor memory set up) as it starts itself, and waits for its predecessor
+// before it touches global memory. Every block waits, so that a kernel's end implies its predecessor's.
+// A call's first kernel is launched plainly.
+__device__ __forceinline__ void linear_follow()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t linear_launch(bool follows, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // lambda = exp(log_decay): -inf (no memory) is taken as exp(-1e4) = 0 so that 0 * log_decay is 0.
 __device__ __forceinline__ float linear_log_decay(const float* log_decay, int h) { return fmaxf(log_decay[h], -1e4f); }

@@ -121,7 +121,7 @@ ssd_status run(const ssd::LinearCall& c, const ssd::LinearScan* s, int n, cudaSt
         return ssd::launch_linear_tc(c, s, n, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
     ssd::LinearCall call = c;
     for (int i = 0; i < n; ++i) {
-        if (ssd::launch_linear_simt(call, s[i], st) != cudaSuccess) return SSD_ERR_CUDA;
+        if (ssd::launch_linear_simt(call, s[i], i > 0, st) != cudaSuccess) return SSD_ERR_CUDA;
         call.clear_status = false;
     }
     return SSD_OK;
@@ -185,7 +185,7 @@ ssd_status ssd_mixer_linear_prefill(const ssd_linear_dims* d, const void* q, int
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, init_state, o, o_ld, final_state, (char*)workspace, w);
     if (d->seqlen <= ssd::kLinearShort) {
         if (ssd::clear_device_status(c.status, st) != cudaSuccess) return SSD_ERR_CUDA;
-        return ssd::launch_linear_short(c, s, false, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+        return ssd::launch_linear_short(c, s, false, false, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
     }
     return run(c, &s, 1, st);
 }
@@ -251,7 +251,7 @@ ssd_status ssd_mixer_linear_decode_step(const ssd_linear_dims* d, const void* q,
     c.log_decay = log_decay;
     c.slot_idx = slot_idx; c.nslots = nslots;
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, state, o, o_ld, state, nullptr, Layout{});
-    return ssd::launch_linear_short(c, s, true, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    return ssd::launch_linear_short(c, s, true, false, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_mixer_linear_backward(const ssd_linear_dims* d, const void* q, int64_t q_ld, const void* k, int64_t k_ld,

@@ -210,14 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const LinearCall& c = a.c;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the compiler sees
     const uint32_t sb = smem_u32(smem);
-    if (c.clear_status && blockIdx.x == 0 && tid == 0) *c.status = kDevOk;
     if (sb & 1023u) {
+        linear_follow();
+        if (c.clear_status && blockIdx.x == 0 && tid == 0) *c.status = kDevOk;
         if (tid == 0) set_device_status(c.status, kDevSmemMisaligned);
         return;
     }
-    // segments of this launch, of every head and scan
-    const int64_t total = (c.list ? (int64_t)c.counts[STATES ? 1 : 0] : c.items) * c.H * a.nscans;
-    if ((int64_t)blockIdx.x >= total) return;
     Work* works = reinterpret_cast<Work*>(smem + C::kOffWork);
     static_assert(C::kOffBar >= C::kOffWork + 2 * sizeof(Work) && C::kOffBar % 8 == 0, "work slots");
     const uint32_t bar0 = sb + C::kOffBar;
@@ -268,6 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    linear_follow();
+    if (c.clear_status && blockIdx.x == 0 && tid == 0) *c.status = kDevOk;
+    // segments of this launch, of every head and scan
+    const int64_t total = (c.list ? (int64_t)c.counts[STATES ? 1 : 0] : c.items) * c.H * a.nscans;
     bool ok = true;
     // The barrier's n-th completion (from 0). A wait tells a completion from the one before it only, so
     // nobody may be two ahead of a wait for it: each barrier's next but one completion needs an arrival
@@ -854,31 +856,30 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, i
 }
 
 template <int DK, int DV, bool STATES>
-cudaError_t launch_one(const TcArgs& a, const TcMaps& m, cudaStream_t st)
+cudaError_t launch_one(const TcArgs& a, const TcMaps& m, bool follows, cudaStream_t st)
 {
     using C = Cfg<DK, DV, STATES>;
     cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<DK, DV, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     LaunchScope ls(STATES ? "linear_tc_states" : "linear_tc", st);
     const int64_t total = a.c.items * a.c.H * a.nscans, sms = device_sm_count();
-    linear_tc_kernel<DK, DV, STATES><<<(unsigned)(total < sms ? total : sms), kThreads, C::kSmem, st>>>(a, m);
-    return cudaGetLastError();
+    return linear_launch(follows, linear_tc_kernel<DK, DV, STATES>, dim3((unsigned)(total < sms ? total : sms)), kThreads, C::kSmem, st, a, m);
 }
 
 template <int DK, int DV>
-cudaError_t launch_shape(const TcArgs& a, const TcMaps& m, cudaStream_t st)
+cudaError_t launch_shape(const TcArgs& a, const TcMaps& m, bool follows, cudaStream_t st)
 {
     if (a.c.split) {
         TcArgs fine = a;
         fine.c = linear_pieces(a.c);
-        cudaError_t e = launch_one<DK, DV, true>(fine, m, st);
+        cudaError_t e = launch_one<DK, DV, true>(fine, m, follows, st);
         for (int i = 0; i < a.nscans && e == cudaSuccess; ++i) e = launch_linear_pass(fine.c, a.s[i], st);
         if (e != cudaSuccess) return e;
         TcArgs after = a;
         after.c.clear_status = false;
-        return launch_one<DK, DV, false>(after, m, st);
+        return launch_one<DK, DV, false>(after, m, true, st);
     }
-    return launch_one<DK, DV, false>(a, m, st);
+    return launch_one<DK, DV, false>(a, m, follows, st);
 }
 
 }  // namespace
@@ -893,7 +894,7 @@ cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int n
     if (c.items == 0) return cudaSuccess;
     if (c.cu_seqlens) {
         cudaError_t e = launch_linear_list(c, st);
-        if (e == cudaSuccess) e = launch_linear_short(c, scans[0], false, st);
+        if (e == cudaSuccess) e = launch_linear_short(c, scans[0], false, true, st);
         if (e != cudaSuccess) return e;
     }
     const bool queue = linear_pieces(c).items * c.H * nscans > device_sm_count();   // of any launch below
@@ -925,8 +926,9 @@ cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int n
                 return cudaErrorInvalidValue;
         }
         const int dk = scans[i].DK, dv = scans[i].DV;
-        const cudaError_t e = dk == 64 ? (dv == 64 ? launch_shape<64, 64>(a, m, st) : launch_shape<64, 128>(a, m, st))
-                                       : (dv == 64 ? launch_shape<128, 64>(a, m, st) : launch_shape<128, 128>(a, m, st));
+        const bool follows = i > 0 || c.list;    // after the call's own kernel
+        const cudaError_t e = dk == 64 ? (dv == 64 ? launch_shape<64, 64>(a, m, follows, st) : launch_shape<64, 128>(a, m, follows, st))
+                                       : (dv == 64 ? launch_shape<128, 64>(a, m, follows, st) : launch_shape<128, 128>(a, m, follows, st));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
