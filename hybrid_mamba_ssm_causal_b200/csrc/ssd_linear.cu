@@ -1,6 +1,8 @@
 // ssd_linear.cu -- linear attention with a decay per head on CUDA cores: the scan for any
 // supported shape and type, the state pass between segments, the sum over shared heads' gradients
 // and the decode step. The tensor-core scan is ssd_linear_tc.cu.
+#include <math.h>
+
 #include <type_traits>
 
 #include "../../include/ssd_mixer.h"
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     constexpr int kPer = (kTileVecs + kThr - 1) / kThr;
     __shared__ __align__(16) T s_in[kTile][2 * DK + DV];      // k, then q, then v
     __shared__ __align__(16) float s_o[kTile][DV];
-    linear_follow();
+    linear_wait();
     if (c.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *c.status = kDevOk;
 
     const int h = blockIdx.x % c.H;
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
             }
         }
     }
+    linear_release();      // not earlier: a successor's blocks, placed beside unfinished ones, crowd some SMs (42 -> 37 us)
     if (s.reverse && it.n > 0) {
 #pragma unroll
         for (int r = 0; r < Sh::kRows; ++r)
@@ -227,9 +230,10 @@ void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, bool foll
 // ------------------------------------------------------------- states between segments
 // Rows of one segment are left alone. Before: seg_states[t] holds piece t's own state from a zero start
 // (the pieces of the scan's last segment have none). After: at each segment's first piece in scan order,
-// the state entering it. A block takes 4096 elements of one (sequence, head); a thread's loads of the
-// next piece are under way while one is added.
-constexpr int kPassElems = 4096;
+// the state entering it. A block takes 1024 elements of one (sequence, head), a thread four of them, with
+// the loads of the next kPassAhead pieces under way: a piece then costs some 0.1 us, with one load ahead
+// it is the load's latency, 0.5.
+constexpr int kPassElems = 1024, kPassAhead = 8;
 __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, const LinearScan s)
 {
     __shared__ LinearItem first;
@@ -252,37 +256,36 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
     const float g = linear_log_decay(c.log_decay, h);
     const bool init = linear_has_init(c, s, seq);
     const float* ip = s.init ? s.init + (first.slot * c.H + h) * (int64_t)hs : nullptr;
-    // pieces in scan order; the short one is the row's last
-    auto at = [&](int64_t k) { return s.seg_states + ((item0 + (s.reverse ? nseg - 1 - k : k)) * c.H + h) * (int64_t)hs; };
-    constexpr int kV = kPassElems / 1024;
-    float4 S[kV], own[kV];
+    if (e0 >= hs) return;
+    // pieces in scan order (the short one is the row's last): p is the present one, `to_start` counts the
+    // pieces to the next one that starts a segment
+    const int64_t step = (s.reverse ? -1 : 1) * (int64_t)c.H * hs;
+    float* p = s.seg_states + ((item0 + (s.reverse ? nseg - 1 : 0)) * c.H + h) * (int64_t)hs + e0;
+    int to_start = 0;
+    const int short_first = s.reverse ? (int)(nseg % c.sub) : 0;    // pieces of the scan's first segment, if not all
+    float4 S = make_float4(0.0f, 0.0f, 0.0f, 0.0f), own[kPassAhead];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-        const int i = e0 + v * 1024;
-        S[v] = own[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (i >= hs) continue;
-        own[v] = *reinterpret_cast<const float4*>(at(0) + i);
-        if (init) {
-            const float* p = ip + (int64_t)(i / s.DK) * s.init_rs + (int64_t)(i % s.DK) * s.init_cs;   // four of one row
-            S[v] = make_float4(p[0], p[s.init_cs], p[2 * s.init_cs], p[3 * s.init_cs]);
-        }
+    for (int x = 0; x < kPassAhead; ++x) own[x] = x < before ? *reinterpret_cast<const float4*>(p + x * step) : S;
+    if (init) {
+        const float* q = ip + (int64_t)(e0 / s.DK) * s.init_rs + (int64_t)(e0 % s.DK) * s.init_cs;   // four of one row
+        S = make_float4(q[0], q[s.init_cs], q[2 * s.init_cs], q[3 * s.init_cs]);
     }
     const LinearDecay whole(g * (float)c.seg_tokens);
-    for (int64_t k = 0; k <= before; ++k) {
-        float4 next[kV];
+    for (int64_t k0 = 0; k0 <= before; k0 += kPassAhead) {
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            next[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (e0 + v * 1024 < hs && k + 1 < before) next[v] = *reinterpret_cast<const float4*>(at(k + 1) + e0 + v * 1024);
-        }
-        const bool starts = s.reverse ? k == 0 || (nseg - 1 - k) % c.sub == c.sub - 1 : k % c.sub == 0;
-        // backwards the short piece comes first (only fixed-length rows run backwards)
-        const LinearDecay d = s.reverse && k == 0 ? LinearDecay(g * (float)(c.L - (nseg - 1) * c.seg_tokens)) : whole;
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            if (starts && e0 + v * 1024 < hs) *reinterpret_cast<float4*>(at(k) + e0 + v * 1024) = S[v];
-            S[v] = make_float4(d.step(S[v].x, own[v].x), d.step(S[v].y, own[v].y), d.step(S[v].z, own[v].z), d.step(S[v].w, own[v].w));
-            own[v] = next[v];
+        for (int x = 0; x < kPassAhead; ++x) {
+            const int64_t k = k0 + x;
+            if (k > before) break;
+            if (to_start == 0) {
+                *reinterpret_cast<float4*>(p) = S;
+                to_start = k == 0 && short_first > 0 ? short_first : c.sub;
+            }
+            --to_start;
+            // backwards the short piece comes first (only fixed-length rows run backwards)
+            const LinearDecay d = s.reverse && k == 0 ? LinearDecay(g * (float)(c.L - (nseg - 1) * c.seg_tokens)) : whole;
+            S = make_float4(d.step(S.x, own[x].x), d.step(S.y, own[x].y), d.step(S.z, own[x].z), d.step(S.w, own[x].w));
+            if (k + kPassAhead < before) own[x] = *reinterpret_cast<const float4*>(p + kPassAhead * step);
+            p += step;
         }
     }
 }
@@ -515,30 +518,29 @@ cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStr
 }
 
 // Splitting rows into segments fills SMs that whole rows would leave idle, at the price of a pass over
-// k and v before the main one and of the segments' states. Times in units of one block of 128 tokens
-// of the main pass. Tensor cores (some 3.3 us a block of 128 x 128): a CTA per SM takes segment after
-// segment, each some 1.8 to start and to end; a block of the states' pass is 0.5; the two more launches
-// 2, and every segment's state goes through memory four times. CUDA cores (token by token, some 20 us a
-// block): two CTAs per SM, one segment each; all the rest is small.
-int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms, int* sub)
+// k and v before the main one and of the segments' states.
+namespace {
+// Tensor cores, in units of one block of 128 tokens of the main pass (some 3.3 us for 128 x 128): a CTA
+// per SM takes segment after segment, each some 1.8 to start and to end; a block of the states' pass is
+// 0.5; the two more launches 2, and every segment's state goes through memory four times.
+int64_t segment_tc(int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms, int* sub)
 {
-    const int64_t rows = b * H * nscans, slots = tc ? sms : 2 * sms;
-    const double start = tc ? 1.8 : 0.2, states = tc ? 0.58 : 0.6, join = tc ? 2.0 : 0.5, each = tc ? 0.01 : 0.003;
+    const int64_t rows = b * H * nscans;
+    const double start = 1.8, states = 0.58, join = 2.0, each = 0.01;
     const int64_t blocks = ((packed ? T : L) + 127) / 128;
-    *sub = 1;
     if (blocks <= 1 || b == 0) return 256;                 // nothing to split: longer than any row
     if (packed && b > 1) {
         // The lengths are not known here. Segments are twice an SM's even share of all blocks (and 8 at
         // least): shorter rows, which find their place among the others, stay whole, and one long prompt
         // among many short rows does not keep a few SMs busy alone.
-        const int64_t share = (blocks * H * nscans + slots - 1) / slots;
+        const int64_t share = (blocks * H * nscans + sms - 1) / sms;
         return (2 * share > 8 ? 2 * share : 8) * 128;
     }
-    const auto rounds = [&](int64_t n) { return (double)((n + slots - 1) / slots); };
+    const auto rounds = [&](int64_t n) { return (double)((n + sms - 1) / sms); };
     double best = rounds(rows) * ((double)blocks + start);   // whole rows
     int64_t best_seg = blocks + 1;
     for (int64_t nseg = 2; nseg <= blocks && nseg <= 256; ++nseg) {
-        for (int m = 1; m <= (tc && !packed ? 4 : 1); ++m) {
+        for (int m = 1; m <= (packed ? 1 : 4); ++m) {
             const int64_t piece = (blocks + nseg * m - 1) / (nseg * m), seg = piece * m;
             const int64_t n = rows * ((blocks + seg - 1) / seg), pieces = (n - rows) * m;
             if (n == rows) continue;
@@ -552,6 +554,52 @@ int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool pac
         }
     }
     return best_seg * 128;
+}
+
+// CUDA cores, in us. A token costs a warp's latency (0.25; states alone 0.12) or, with w warps to a
+// scheduler, w times its issue slots (0.066 + 0.0004 dk; states half of it), and a little more where the two
+// are near: so segments are cut until the schedulers have some three warps each. A CTA's state comes and goes
+// at some 15 KB a us of its SM; the pass that joins the segments takes 0.07 a segment of a row.
+int64_t segment_simt(int64_t b, int64_t L, int64_t T, bool packed, int H, int DK, int DV, int sms)
+{
+    const int64_t tiles = ((packed ? T : L) + kTile - 1) / kTile;
+    if (tiles <= 1 || b == 0) return 2 * kTile;
+    const int rows_per_warp = DK == 16 ? 16 : 8;
+    const double warps = DV > rows_per_warp ? DV / rows_per_warp : 1, slots = 0.066 + 0.0004 * DK;
+    const double state_kb = 4.0 * DK * DV / 1024.0;
+    const auto pass = [&](int64_t n, double seg, double latency, double issue) {
+        // a few CTAs to an SM: the fullest SM counts; many: their average
+        const double each = n > 8 * (int64_t)sms ? (double)n / sms : (double)((n + sms - 1) / sms), w = each * warps / 4.0;
+        return 3.0 + each * state_kb / 15.0 + seg * kTile * pow(pow(latency, 4.0) + pow(w * issue, 4.0), 0.25);
+    };
+    if (packed && b > 1) {
+        // The lengths are not known here: an SM's even share of all tokens with three warps to a
+        // scheduler, and 64 tokens at least.
+        const double ctas = sms * (12.0 / warps > 1.0 ? 12.0 / warps : 1.0);
+        const int64_t share = (int64_t)((double)tiles * H / ctas) + 1;
+        return (share > 4 ? share : 4) * kTile;
+    }
+    const int64_t rows = b * H;
+    double best = pass(rows, (double)tiles, 0.25, slots);    // whole rows
+    int64_t best_seg = tiles + 1;
+    for (int64_t nseg = 2; nseg <= tiles && nseg <= 512; ++nseg) {
+        const int64_t seg = (tiles + nseg - 1) / nseg, n = rows * ((tiles + seg - 1) / seg);
+        const double cost = pass(n, (double)seg, 0.25, slots) + pass(n - rows, (double)seg, 0.12, 0.5 * slots) +
+                            3.0 + 0.07 * (double)nseg + 2.0 * state_kb * (double)n / 6400.0;
+        if (cost < best) {
+            best = cost;
+            best_seg = seg;
+        }
+    }
+    return best_seg * kTile;
+}
+}  // namespace
+
+int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int DK, int DV, int sms,
+                              int* sub)
+{
+    *sub = 1;
+    return tc ? segment_tc(b, L, T, packed, H, nscans, sms, sub) : segment_simt(b, L, T, packed, H, DK, DV, sms);
 }
 
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,

@@ -94,18 +94,21 @@ cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st);
 // `follows`: it comes after another kernel of the call.
 cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool one, bool follows, cudaStream_t st);
 // Segment length of a call's scans, and the pieces of a segment in the states' pass.
-int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms, int* sub);
+int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int DK, int DV, int sms,
+                              int* sub);
 
 #ifdef __CUDACC__
 
 // A call's kernels follow one another by programmatic dependent launch: each lets its successor start
 // (blocks placed, shared and tensor memory set up) as it starts itself, and waits for its predecessor
-// before it touches global memory. Every block waits, so that a kernel's end implies its predecessor's.
-// A call's first kernel is launched plainly.
+// before it touches global memory (the scan on CUDA cores lets it start later). Every block waits, so that
+// a kernel's end implies its predecessor's. A call's first kernel is launched plainly.
+__device__ __forceinline__ void linear_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void linear_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void linear_follow()
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    linear_release();
+    linear_wait();
 }
 template <typename... P, typename... A>
 cudaError_t linear_launch(bool follows, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args)

@@ -69,7 +69,7 @@ void plan(ssd::LinearCall* c, const ssd_linear_dims* d, bool packed, int nscans)
     c->act = d->act;
     // on CUDA cores the scans of a backward pass run one after another
     c->seg_tokens = ssd::linear_segment_tokens(on_tensor_cores(d), d->batch, c->L, c->T, packed, d->nheads,
-                                               on_tensor_cores(d) ? nscans : 1, ssd::device_sm_count(), &c->sub);
+                                               on_tensor_cores(d) ? nscans : 1, d->dk, d->dv, ssd::device_sm_count(), &c->sub);
     if (packed) {
         c->nseg = 0;
         c->items = d->batch > 0 ? d->batch + c->T / c->seg_tokens : 0;
