@@ -9,9 +9,14 @@
 #include "ssd_common.cuh"
 #include "ssd_linear.h"
 #include "ssd_profile.h"
+#include "ssd_tc_util.cuh"
 
 namespace ssd {
 namespace {
+
+using tc::fma2;
+using tc::mul2;
+using tc::splat2;
 
 // ---------------------------------------------------------------------------- the scan
 // Token by token: the recurrence needs 4 DK DV flops a token, fewer than any chunked form, and
@@ -29,6 +34,46 @@ struct SimtShape {
     static constexpr int kRows = 8;                           // state rows per lane
     static constexpr int kWarpRows = kRows * (32 / kLanes);
 };
+
+// N neighbouring values of a row in shared memory, aligned to their own size
+template <int N>
+__device__ __forceinline__ void load_row(const float* p, float* out)
+{
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p + i);
+            out[i] = x.x; out[i + 1] = x.y; out[i + 2] = x.z; out[i + 3] = x.w;
+        }
+    } else if constexpr (N == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        out[0] = x.x; out[1] = x.y;
+    } else {
+        out[0] = *p;
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float* out)
+{
+    uint32_t w[N > 1 ? N / 2 : 1];
+    if constexpr (N == 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if constexpr (N == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x; w[1] = x.y;
+    } else if constexpr (N == 2) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+        out[0] = __bfloat162float(*p);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        out[2 * i] = __uint_as_float(w[i] << 16);
+        out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
 
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV / SimtShape<DK>::kWarpRows : 1))
@@ -61,24 +106,25 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     const LinearDecay decay(linear_log_decay(c.log_decay, h));
     const int64_t hs = (int64_t)DK * DV;
 
-    float S[Sh::kRows][Sh::kCols];
+    constexpr int kPairs = Sh::kRows / 2;
+    float2 S[kPairs][Sh::kCols];             // two neighbouring rows in a pair: two roundings an instruction
 #pragma unroll
-    for (int r = 0; r < Sh::kRows; ++r)
+    for (int r = 0; r < kPairs; ++r)
 #pragma unroll
-        for (int e = 0; e < Sh::kCols; ++e) S[r][e] = 0.0f;
+        for (int e = 0; e < Sh::kCols; ++e) S[r][e] = splat2(0.0f);
     if (!state_only) {
         if (it.nseg > 1) {   // never the slot itself: the row's last segment may be rewriting it
             const float* p = s.seg_states + (item * c.H + h) * hs;
 #pragma unroll
-            for (int r = 0; r < Sh::kRows; ++r)
+            for (int r = 0; r < kPairs; ++r)
 #pragma unroll
-                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = p[(d0 + r) * DK + e0 + e];
+                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = make_float2(p[(d0 + 2 * r) * DK + e0 + e], p[(d0 + 2 * r + 1) * DK + e0 + e]);
         } else if (linear_has_init(c, s, it.seq)) {
             const float* p = s.init + (it.slot * c.H + h) * hs;
 #pragma unroll
-            for (int r = 0; r < Sh::kRows; ++r)
+            for (int r = 0; r < kPairs; ++r)
 #pragma unroll
-                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = p[(d0 + r) * s.init_rs + (e0 + e) * s.init_cs];
+                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = make_float2(p[(d0 + 2 * r) * s.init_rs + (e0 + e) * s.init_cs], p[(d0 + 2 * r + 1) * s.init_rs + (e0 + e) * s.init_cs]);
         }
     }
 
@@ -121,24 +167,27 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
         const auto token = [&](int tt, auto slow_c, float f) {
             constexpr bool slow = decltype(slow_c)::value;
             float kk[Sh::kCols], v[Sh::kRows];
+            load_row<Sh::kCols>(&s_in[tt][e0], kk);
+            load_row<Sh::kRows>(&s_in[tt][2 * DK + d0], v);
 #pragma unroll
-            for (int e = 0; e < Sh::kCols; ++e) kk[e] = ld_f(&s_in[tt][e0 + e]);
+            for (int e = 0; e < Sh::kCols; ++e) {
+                const float2 ke = splat2(s.u_scale * kk[e]), ff = splat2(f);
 #pragma unroll
-            for (int r = 0; r < Sh::kRows; ++r) v[r] = s.u_scale * ld_f(&s_in[tt][2 * DK + d0 + r]);
-#pragma unroll
-            for (int r = 0; r < Sh::kRows; ++r)
-#pragma unroll
-                for (int e = 0; e < Sh::kCols; ++e)
-                    S[r][e] = slow ? fmaf(f, S[r][e], fmaf(v[r], kk[e], S[r][e])) : fmaf(f, S[r][e], v[r] * kk[e]);
+                for (int r = 0; r < kPairs; ++r) {
+                    const float2 vr = make_float2(v[2 * r], v[2 * r + 1]);
+                    S[r][e] = slow ? fma2(ff, S[r][e], fma2(vr, ke, S[r][e])) : fma2(ff, S[r][e], mul2(vr, ke));
+                }
+            }
             if (!state_only) {
-                float o[Sh::kRows];
+                float qq[Sh::kCols], o[Sh::kRows];
+                load_row<Sh::kCols>(&s_in[tt][DK + e0], qq);
 #pragma unroll
-                for (int r = 0; r < Sh::kRows; ++r) o[r] = 0.0f;
+                for (int r = 0; r < kPairs; ++r) {
+                    float2 x = mul2(S[r][0], splat2(qq[0]));
 #pragma unroll
-                for (int e = 0; e < Sh::kCols; ++e) {
-                    const float qq = ld_f(&s_in[tt][DK + e0 + e]);
-#pragma unroll
-                    for (int r = 0; r < Sh::kRows; ++r) o[r] = fmaf(S[r][e], qq, o[r]);
+                    for (int e = 1; e < Sh::kCols; ++e) x = fma2(S[r][e], splat2(qq[e]), x);
+                    o[2 * r] = x.x;
+                    o[2 * r + 1] = x.y;
                 }
                 // lanes with the offset's bit set keep the upper half of the rows, the others the lower
                 int row = 0;
@@ -184,18 +233,21 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     linear_release();      // not earlier: a successor's blocks, placed beside unfinished ones, crowd some SMs (42 -> 37 us)
     if (s.reverse && it.n > 0) {
 #pragma unroll
-        for (int r = 0; r < Sh::kRows; ++r)
+        for (int r = 0; r < kPairs; ++r)
 #pragma unroll
-            for (int e = 0; e < Sh::kCols; ++e) S[r][e] = decay.step(S[r][e], 0.0f);
+            for (int e = 0; e < Sh::kCols; ++e) S[r][e] = make_float2(decay.step(S[r][e].x, 0.0f), decay.step(S[r][e].y, 0.0f));
     }
     float* out = nullptr;
     if (state_only) out = s.seg_states + (item * c.H + h) * hs;
     else if (last && s.final_state) out = s.final_state + (it.slot * c.H + h) * hs;
     if (out) {
 #pragma unroll
-        for (int r = 0; r < Sh::kRows; ++r)
+        for (int r = 0; r < kPairs; ++r)
 #pragma unroll
-            for (int e = 0; e < Sh::kCols; ++e) out[(d0 + r) * DK + e0 + e] = S[r][e];
+            for (int e = 0; e < Sh::kCols; ++e) {
+                out[(d0 + 2 * r) * DK + e0 + e] = S[r][e].x;
+                out[(d0 + 2 * r + 1) * DK + e0 + e] = S[r][e].y;
+            }
     }
 }
 
