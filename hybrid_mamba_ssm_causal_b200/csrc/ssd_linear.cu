@@ -25,6 +25,9 @@ using tc::splat2;
 // in registers, its lanes along DK. Tokens come in tiles of 16 through shared memory, the next
 // tile's loads in flight while the present one is used. The products S q are summed over the lanes
 // by a butterfly that halves the values with each of its first three steps (9 shuffles for 8 rows).
+// A token takes a warp 0.25 us (its chain of loads, sums and shuffles) and, from some three warps to a
+// scheduler on, issue slots and the pipe that shared loads and shuffles have in common: 2 x 777 x 12 heads
+// 64 x 32 fp32 34 us, 1 x 16384 x 32 heads of 128 2.6 ms (18 % of the rate of fp32 products).
 constexpr int kTile = 16;
 
 template <int DK>
@@ -283,18 +286,42 @@ void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, bool foll
 // Rows of one segment are left alone. Before: seg_states[t] holds piece t's own state from a zero start
 // (the pieces of the scan's last segment have none). After: at each segment's first piece in scan order,
 // the state entering it. A block takes 1024 elements of one (sequence, head), a thread four of them, with
-// the loads of the next kPassAhead pieces under way: a piece then costs some 0.1 us, with one load ahead
+// the loads of the next kPassAhead pieces under way: a piece then costs 0.07 us, with one load ahead
 // it is the load's latency, 0.5.
 constexpr int kPassElems = 1024, kPassAhead = 8;
+// The n-th of a packed call's sequences that have more than one segment (of which there are at most
+// T / seg_tokens), found by a block of 256 threads; false: there is none.
+__device__ bool nth_long(const LinearCall& c, int n, int64_t* seq)
+{
+    __shared__ int longs[8], found;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int64_t base = 0; base < c.b && n >= 0; base += 256) {
+        const int64_t i = base + threadIdx.x;
+        const bool is = i < c.b && (int64_t)c.cu_seqlens[i + 1] - c.cu_seqlens[i] > c.seg_tokens;
+        const unsigned all = __ballot_sync(0xffffffffu, is);
+        if (lane == 0) longs[warp] = __popc(all);
+        __syncthreads();
+        int before = __popc(all & ((1u << lane) - 1)), total = 0;
+        for (int w = 0; w < 8; ++w) {
+            before += w < warp ? longs[w] : 0;
+            total += longs[w];
+        }
+        if (is && before == n) found = (int)i;
+        n -= total;
+        __syncthreads();
+    }
+    *seq = found;
+    return n < 0;
+}
 __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, const LinearScan s)
 {
     __shared__ LinearItem first;
     __shared__ int64_t item0;
     const int h = blockIdx.y;
-    const int64_t seq = blockIdx.z;
+    int64_t seq = blockIdx.z;
     const int hs = s.DK * s.DV, e0 = blockIdx.x * kPassElems + 4 * threadIdx.x;
     linear_follow();
-    if (c.cu_seqlens && (int64_t)c.cu_seqlens[seq + 1] - c.cu_seqlens[seq] <= c.seg_tokens) return;
+    if (c.cu_seqlens && !nth_long(c, blockIdx.z, &seq)) return;
     if (threadIdx.x == 0) {
         item0 = c.cu_seqlens ? linear_packed_first(c, seq) : seq * c.nseg;
         const bool is = c.cu_seqlens ? linear_packed_item(c, seq, 0, &first) : linear_item(c, item0, &first);
@@ -418,7 +445,7 @@ __global__ void __launch_bounds__(kListThreads) linear_list_kernel(const LinearC
 // Up to kLinearShort tokens of each row, token by token: the fp32 state is read once and written once,
 // which for a few tokens is nearly all of the bytes. Lanes along DK (a float4 each), kRif state rows in
 // flight per lane, so a CTA's whole part of the state is on its way before the first product.
-// 256 sequences of 128 heads of 128 x 64: 341 us a step, 6.3 TB/s.
+// 256 sequences of 128 heads of 128 x 64: 323 us a step, 6.7 TB/s; one token of 32 heads of 128: 2.7 us.
 constexpr int kShortThreads = 128, kRif = 8;
 
 struct LinearShort {
@@ -433,6 +460,7 @@ struct LinearShort {
     void* o;
     int H, share, DV, parts;
     float scale;
+    int* status;                // cleared by the kernel where it is the call's only one
 };
 
 template <typename T>
@@ -452,9 +480,11 @@ template <typename T, int DK, bool ONE>
 __global__ void __launch_bounds__(kShortThreads) linear_short_kernel(const LinearShort p)
 {
     constexpr int kLanes = DK / 4, kRows = kShortThreads / kLanes;   // rows of one pass of the CTA
+    constexpr int kTokens = ONE ? 1 : kLinearShort;
     const int64_t seq = blockIdx.y;
     const int h = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
     if (!ONE) linear_follow();
+    if (!ONE && p.status && blockIdx.x == 0 && seq == 0 && threadIdx.x == 0) *p.status = kDevOk;
     int64_t row = seq * p.L, n = p.L;
     if (!ONE && p.cu_seqlens) {
         row = p.cu_seqlens[seq];
@@ -476,47 +506,66 @@ __global__ void __launch_bounds__(kShortThreads) linear_short_kernel(const Linea
         if (init && r < p.DV) s[i] = *reinterpret_cast<const float4*>(p.init + at + (int64_t)r * DK);
     }
     const LinearDecay decay(linear_log_decay(p.log_decay, h));
-    const T* kp = (const T*)p.k + row * p.k_ld + (int64_t)(h / p.share) * DK + 4 * l;
-    const T* qp = (const T*)p.q + row * p.q_ld + (int64_t)h * DK + 4 * l;
+    const T* kp = (const T*)p.k + row * p.k_ld + (int64_t)(h / p.share) * DK;
+    const T* qp = (const T*)p.q + row * p.q_ld + (int64_t)h * DK;
     const T* vp = (const T*)p.v + row * p.v_ld + (int64_t)(h / p.share) * p.DV;
     T* op = (T*)p.o + row * p.o_ld + (int64_t)h * p.DV;
-    // a token's k, q and v are loaded while the one before is worked on
-    float4 k_next = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q_next = k_next;
-    float v_next[kRif];
-    auto fetch = [&]() {
-        k_next = load4(kp);
-        q_next = load4(qp);
-#pragma unroll
-        for (int i = 0; i < kRif; ++i) v_next[i] = r0 + i * kRows < p.DV ? ld_f(vp + r0 + i * kRows) : 0.0f;
-        kp += p.k_ld;
-        qp += p.q_ld;
-        vp += p.v_ld;
-    };
-    if (ONE || n > 0) fetch();
+    // several tokens come into shared memory together, with the state's loads: token after token from
+    // global memory is a load's latency each (1.4 us)
+    __shared__ __align__(16) float sk[kTokens][DK], sq[kTokens][DK], sv[kTokens][kRows * kRif];
+    if (!ONE) {
+        for (int id = threadIdx.x; id < (int)n * kLanes; id += kShortThreads) {
+            const int t = id / kLanes, e = id % kLanes * 4;
+            *reinterpret_cast<float4*>(&sk[t][e]) = load4(kp + t * p.k_ld + e);
+            *reinterpret_cast<float4*>(&sq[t][e]) = load4(qp + t * p.q_ld + e);
+        }
+        const int v0 = part * kRows * kRif, vecs = (p.DV - v0 < kRows * kRif ? p.DV - v0 : kRows * kRif) / 4;
+        for (int id = threadIdx.x; id < (int)n * vecs; id += kShortThreads) {
+            const int t = id / vecs, e = id % vecs * 4;
+            *reinterpret_cast<float4*>(&sv[t][e]) = load4(vp + t * p.v_ld + v0 + e);
+        }
+        __syncthreads();
+    }
 #pragma unroll 1
-    for (int64_t t = 0; t < (ONE ? 1 : n); ++t) {
-        const float4 k = k_next, q = q_next;
-        float vv[kRif];
-#pragma unroll
-        for (int i = 0; i < kRif; ++i) vv[i] = v_next[i];
-        if (!ONE && t + 1 < n) fetch();
+    for (int t = 0; t < (ONE ? 1 : (int)n); ++t) {
+        const float4 k = ONE ? load4(kp + 4 * l) : *reinterpret_cast<const float4*>(&sk[t][4 * l]);
+        const float4 q = ONE ? load4(qp + 4 * l) : *reinterpret_cast<const float4*>(&sq[t][4 * l]);
+        float o[kRif];
 #pragma unroll
         for (int i = 0; i < kRif; ++i) {
             const int r = r0 + i * kRows;
-            const bool in = r < p.DV;
-            float o = 0.0f;
-            if (in) {
-                const float v = vv[i];
+            o[i] = 0.0f;
+            if (r < p.DV) {
+                const float v = ONE ? ld_f(vp + r) : sv[t][threadIdx.x / kLanes + i * kRows];
                 s[i].x = decay.step(s[i].x, v * k.x);
                 s[i].y = decay.step(s[i].y, v * k.y);
                 s[i].z = decay.step(s[i].z, v * k.z);
                 s[i].w = decay.step(s[i].w, v * k.w);
-                o = s[i].x * q.x + s[i].y * q.y + s[i].z * q.z + s[i].w * q.w;
+                o[i] = s[i].x * q.x + s[i].y * q.y + s[i].z * q.z + s[i].w * q.w;
                 if (ONE) *reinterpret_cast<float4*>(p.final_state + at + (int64_t)r * DK) = s[i];
             }
+        }
+        // lanes with the offset's bit set keep the upper half of the rows, the others the lower
+        int first = 0;
 #pragma unroll
-            for (int off = kLanes / 2; off > 0; off >>= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
-            if (in && l == 0) op[r] = Act<T>::from_f(p.scale * o);
+        for (int half = kRif / 2, off = kLanes / 2; half > 0 && off > 0; half >>= 1, off >>= 1) {
+            const bool up = (l & off) != 0;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const float give = up ? o[i] : o[i + half];
+                const float keep = up ? o[i + half] : o[i];
+                o[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+            first += up ? half : 0;
+        }
+#pragma unroll
+        for (int off = kLanes / 16; off > 0; off >>= 1) o[0] += __shfl_xor_sync(0xffffffffu, o[0], off);
+        if (kLanes <= 8 || (l & (kLanes / 8 - 1)) == 0) {
+#pragma unroll
+            for (int i = 0; i < (kLanes < 8 ? 8 / kLanes : 1); ++i) {
+                const int r = r0 + (first + i) * kRows;
+                if (r < p.DV) op[r] = Act<T>::from_f(p.scale * o[i]);
+            }
         }
         op += p.o_ld;
     }
@@ -565,7 +614,8 @@ cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, bool fo
 cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st)
 {
     LaunchScope ls("linear_pass", st);
-    return linear_launch(true, linear_pass_kernel, dim3((unsigned)((s.DK * s.DV + kPassElems - 1) / kPassElems), (unsigned)c.H, (unsigned)c.b),
+    const int64_t rows = c.cu_seqlens && c.T / c.seg_tokens < c.b ? c.T / c.seg_tokens : c.b;
+    return linear_launch(true, linear_pass_kernel, dim3((unsigned)((s.DK * s.DV + kPassElems - 1) / kPassElems), (unsigned)c.H, (unsigned)rows),
                          256, 0, st, c, s);
 }
 
@@ -684,6 +734,7 @@ cudaError_t launch_linear_short(const LinearCall& c, const LinearScan& s, bool o
     p.nslots = c.nslots; p.L = c.L; p.T = c.T;
     p.H = c.H; p.share = s.k_share; p.DV = s.DV;
     p.scale = s.out_scale;
+    p.status = c.clear_status && !c.cu_seqlens ? c.status : nullptr;
     if (c.act == SSD_BF16)
         return one ? launch_short<__nv_bfloat16, true>(p, s.DK, c.b, follows, st) : launch_short<__nv_bfloat16, false>(p, s.DK, c.b, follows, st);
     return one ? launch_short<float, true>(p, s.DK, c.b, follows, st) : launch_short<float, false>(p, s.DK, c.b, follows, st);

@@ -183,10 +183,8 @@ ssd_status ssd_mixer_linear_prefill(const ssd_linear_dims* d, const void* q, int
     c.taken = c.status + 1;
     c.clear_status = true;
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, init_state, o, o_ld, final_state, (char*)workspace, w);
-    if (d->seqlen <= ssd::kLinearShort) {
-        if (ssd::clear_device_status(c.status, st) != cudaSuccess) return SSD_ERR_CUDA;
+    if (d->seqlen <= ssd::kLinearShort)
         return ssd::launch_linear_short(c, s, false, false, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
-    }
     return run(c, &s, 1, st);
 }
 
