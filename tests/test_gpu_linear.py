@@ -349,6 +349,38 @@ def test_nan_stays_in_its_row_and_its_future(act, shape):
     assert bool(o[0, t:].isnan().any(-1).all()) and bool(fs[0].isnan().any()) and not bool(fs[1].isnan().any())
 
 
+@pytest.mark.parametrize("act,shape", [("bf16", (3, 200, 2, 2, 64, 128)), ("bf16", (3, 300, 2, 1, 128, 64)), ("f32", (3, 45, 2, 2, 32, 32)),
+                                       ("bf16", (3, 6, 2, 1, 64, 64))])
+def test_nan_of_a_row_stays_out_of_its_neighbours(act, shape):
+    """Everything of the middle row is NaN: its neighbours' outputs, states and gradients are as without it
+    (the last block of a row is filled up with the next one's tokens)."""
+    d = dims(*shape, act)
+    x = make(*shape, act, seed=8)
+    y = {n: t if n == "log_decay" else t.clone() for n, t in x.items()}
+    for n in ("q", "k", "v", "do", "init", "dfinal"):
+        y[n][1] = float("nan")
+    both = [(*forward(z, d), *sm.linear_backward(d, z["q"], z["k"], z["v"], z["log_decay"], z["do"], z["init"], z["dfinal"]).values())
+            for z in (x, y)]
+    for clean, got in zip(*both):
+        assert torch.equal(got[::2], clean[::2]) and not bool(clean.isnan().any())
+        assert bool(got[1].isnan().any())
+
+
+@pytest.mark.parametrize("act,dk,dv", [("bf16", 64, 64), ("f32", 16, 32)])
+def test_packed_without_any_token(act, dk, dv):
+    """No token rows at all: slots keep their states, or become zeros where nothing is continued."""
+    d = dims(3, 0, 2, 2, dk, dv, act)
+    q = torch.empty(0, 2 * dk, dtype=d.torch_dtype, device="cuda")
+    v = torch.empty(0, 2 * dv, dtype=d.torch_dtype, device="cuda")
+    state = torch.randn(4, 2, dv, dk, device="cuda")
+    before = state.clone()
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    o = sm.linear_prefill_varlen(d, cu, torch.tensor([2, 0, 3], dtype=torch.int32, device="cuda"),
+                                 torch.tensor([1, 0, 1], dtype=torch.uint8, device="cuda"), q, q, v, torch.zeros(2, device="cuda"), state)
+    before[0] = 0.0
+    assert o.shape == (0, 2 * dv) and torch.equal(state, before)
+
+
 def test_the_binding_checks_types_shapes_and_rows():
     shape = (2, 64, 2, 2, 64, 64)
     d = dims(*shape, "bf16")
