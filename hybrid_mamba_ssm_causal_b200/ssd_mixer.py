@@ -595,17 +595,21 @@ def decode_step(dims: Dims, x, z, B, C, dt, A, D, conv_w, conv_b, dt_bias, norm_
 
 
 # ------------------------------------------------------- linear attention and layer norm
-def _rows_on(t, name: str, rows: int, width: int, dtype, dev):
-    """Pointer and row stride of `rows` evenly strided rows of `width` unit-stride elements, of the
-    given type and on the given device. Dimensions of size 1 set no stride."""
+def _refuse(t, name: str, dtype, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+    raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+
+
+def _rows_on(t, name: str, rows: int, width: int, dtype, dev):
+    """Pointer and row stride of `rows` evenly strided rows of `width` unit-stride elements, of the
+    given type and on the given device. Dimensions of size 1 set no stride."""
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dtype:
+        _refuse(t, name, dtype, dev)
     shape = t.shape
-    if t.dim() < 1 or shape[-1] != width or t.numel() != rows * width:
+    if not shape or shape[-1] != width or t.numel() != rows * width:
         raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(shape)}")
     if rows == 0 or t.is_contiguous():
         return t.data_ptr(), width
@@ -629,17 +633,18 @@ def _whole(t, name: str, shape, dtype, dev):
     """Pointer of a contiguous tensor of exactly this shape, type and device (None: NULL)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call on {dev}")
-    if tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dtype:
+        _refuse(t, name, dtype, dev)
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _new_like(t):
+    """A contiguous tensor of t's shape and type (empty_like keeps a dense tensor's other orders)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _device_of(t, name: str):
@@ -735,10 +740,11 @@ def linear_prefill(dims: LinearDims, q, k, v, log_decay, init_state=None, worksp
         if out is None:
             o = q.new_empty((b, L, H * dims.dv))
             fs = log_decay.new_empty(sshape)
+            po, pf = (o.data_ptr(), H * dims.dv), fs.data_ptr()
         else:
             o, fs = out
-        po = _rows_on(o, "o", b * L, H * dims.dv, dims.torch_dtype, dev)
-        pf = _whole(fs, "final_state", sshape, torch.float32, dev)
+            po = _rows_on(o, "o", b * L, H * dims.dv, dims.torch_dtype, dev)
+            pf = _whole(fs, "final_state", sshape, torch.float32, dev)
         pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
                                 lib.ssd_mixer_linear_prefill_workspace_size(ctypes.byref(cd)), "linear_prefill", dev)
         st = lib.ssd_mixer_linear_prefill(ctypes.byref(cd), *rows, pd, pi, *po, pf, pw, nw, on)
@@ -765,7 +771,9 @@ def linear_prefill_varlen(dims: LinearDims, cu_seqlens, slot_idx, has_init, q, k
     with _On(dev, stream) as on:
         if o is None:
             o = q.new_empty((T, H * dims.dv))
-        po = _rows_on(o, "o", T, H * dims.dv, dims.torch_dtype, dev)
+            po = o.data_ptr(), H * dims.dv
+        else:
+            po = _rows_on(o, "o", T, H * dims.dv, dims.torch_dtype, dev)
         pw, nw, ws = _workspace(workspace, 0 if workspace is not None else
                                 lib.ssd_mixer_linear_prefill_varlen_workspace_size(ctypes.byref(cd)),
                                 "linear_prefill_varlen", dev)
@@ -789,7 +797,9 @@ def linear_decode_step(dims: LinearDims, q, k, v, log_decay, state, slot_idx=Non
     with _On(dev, stream) as on:
         if o is None:
             o = q.new_empty((b, H * dims.dv))
-        po = _rows_on(o, "o", b, H * dims.dv, dims.torch_dtype, dev)
+            po = o.data_ptr(), H * dims.dv
+        else:
+            po = _rows_on(o, "o", b, H * dims.dv, dims.torch_dtype, dev)
         st = load_library().ssd_mixer_linear_decode_step(ctypes.byref(cd), *rows, pd, ps, nslots, psl, *po, on)
     _check(st, "ssd_mixer_linear_decode_step")
     return o
@@ -842,14 +852,16 @@ def layer_norm(x, weight=None, bias=None, groups: int = 1, eps: float = 1e-5, ou
     pw = _whole(weight, "weight", (C,), torch.float32, dev)
     pb = _whole(bias, "bias", (C,), torch.float32, dev)
     with _On(dev, stream) as on:
-        y = x.new_empty(x.shape) if out is None else out
-        py = _rows_on(y, "out", rows, C, x.dtype, dev)
-        stats = x.new_empty((2, *x.shape[:-1], groups), dtype=torch.float32)
-        pm = stats.data_ptr()
-        st = load_library().ssd_mixer_layer_norm(rows, groups, width, eps, act, *px, pw, pb, *py, pm,
-                                                 pm + 4 * rows * groups, on)
+        if out is None:
+            y = _new_like(x)
+            py = y.data_ptr(), C
+        else:
+            y, py = out, _rows_on(out, "out", rows, C, x.dtype, dev)
+        mean = x.new_empty((*x.shape[:-1], groups), dtype=torch.float32)
+        rstd = torch.empty_like(mean)
+        st = load_library().ssd_mixer_layer_norm(rows, groups, width, eps, act, *px, pw, pb, *py, mean.data_ptr(),
+                                                 rstd.data_ptr(), on)
     _check(st, "ssd_mixer_layer_norm")
-    mean, rstd = stats.unbind(0)
     return y, mean, rstd
 
 
@@ -868,14 +880,13 @@ def layer_norm_backward(dy, x, weight, mean, rstd, groups: int = 1, workspace=No
     pm, pr = _whole(mean, "mean", sshape, torch.float32, dev), _whole(rstd, "rstd", sshape, torch.float32, dev)
     lib = load_library()
     with _On(dev, stream) as on:
-        dx = x.new_empty(x.shape)
-        dpar = x.new_empty((2, C), dtype=torch.float32)
-        pp = dpar.data_ptr()
+        dx = _new_like(x)
+        dweight = x.new_empty((C,), dtype=torch.float32) if weight is None else torch.empty_like(weight)
+        dbias = torch.empty_like(dweight)
         pws, nws, ws = _workspace(workspace, 0 if workspace is not None else
                                   lib.ssd_mixer_layer_norm_backward_workspace_size(rows, groups, width, act),
                                   "layer_norm_backward", dev)
-        st = lib.ssd_mixer_layer_norm_backward(rows, groups, width, act, *pdy, *px, pw, pm, pr, dx.data_ptr(), C, pp,
-                                               pp + 4 * C, pws, nws, on)
+        st = lib.ssd_mixer_layer_norm_backward(rows, groups, width, act, *pdy, *px, pw, pm, pr, dx.data_ptr(), C,
+                                               dweight.data_ptr(), dbias.data_ptr(), pws, nws, on)
     _check(st, "ssd_mixer_layer_norm_backward")
-    dweight, dbias = dpar.unbind(0)
     return dx, dweight, dbias
