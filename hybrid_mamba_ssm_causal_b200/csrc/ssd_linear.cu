@@ -80,8 +80,9 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float* out)
 
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV / SimtShape<DK>::kWarpRows : 1))
-    linear_scan_kernel(const LinearCall c, const LinearScan s, bool state_only)
+    linear_scan_kernel(const LinearCall c, const LinearScans scans, bool state_only)
 {
+    const LinearScan& s = scans.s[blockIdx.y];
     using Sh = SimtShape<DK>;
     constexpr int kWarps = DV / Sh::kWarpRows > 0 ? DV / Sh::kWarpRows : 1;
     constexpr int kThr = 32 * kWarps;
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     __shared__ __align__(16) T s_in[kTile][2 * DK + DV];      // k, then q, then v
     __shared__ __align__(16) float s_o[kTile][DV];
     linear_wait();
-    if (c.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *c.status = kDevOk;
+    if (c.clear_status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *c.status = kDevOk;
 
     const int h = blockIdx.x % c.H;
     const int64_t item = blockIdx.x / c.H;
@@ -255,16 +256,17 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
 }
 
 template <typename T, int DK, int DV>
-void launch_scan_shape(const LinearCall& c, const LinearScan& s, bool state_only, bool follows, cudaStream_t st)
+void launch_scan_shape(const LinearCall& c, const LinearScans& s, bool state_only, bool follows, cudaStream_t st)
 {
     constexpr int kWarps = DV / SimtShape<DK>::kWarpRows > 0 ? DV / SimtShape<DK>::kWarpRows : 1;
     LaunchScope ls(state_only ? "linear_states" : "linear_scan", st);
-    linear_launch(follows, linear_scan_kernel<T, DK, DV>, dim3((unsigned)(c.items * c.H)), 32 * kWarps, 0, st, c, s, state_only);
+    linear_launch(follows, linear_scan_kernel<T, DK, DV>, dim3((unsigned)(c.items * c.H), (unsigned)s.n), 32 * kWarps, 0,
+                  st, c, s, state_only);
 }
 template <typename T, int DK>
-void launch_scan_dv(const LinearCall& c, const LinearScan& s, bool so, bool follows, cudaStream_t st)
+void launch_scan_dv(const LinearCall& c, const LinearScans& s, bool so, bool follows, cudaStream_t st)
 {
-    switch (s.DV) {
+    switch (s.s[0].DV) {
     case 16: return launch_scan_shape<T, DK, 16>(c, s, so, follows, st);
     case 32: return launch_scan_shape<T, DK, 32>(c, s, so, follows, st);
     case 64: return launch_scan_shape<T, DK, 64>(c, s, so, follows, st);
@@ -272,9 +274,9 @@ void launch_scan_dv(const LinearCall& c, const LinearScan& s, bool so, bool foll
     }
 }
 template <typename T>
-void launch_scan_dk(const LinearCall& c, const LinearScan& s, bool so, bool follows, cudaStream_t st)
+void launch_scan_dk(const LinearCall& c, const LinearScans& s, bool so, bool follows, cudaStream_t st)
 {
-    switch (s.DK) {
+    switch (s.s[0].DK) {
     case 16: return launch_scan_dv<T, 16>(c, s, so, follows, st);
     case 32: return launch_scan_dv<T, 32>(c, s, so, follows, st);
     case 64: return launch_scan_dv<T, 64>(c, s, so, follows, st);
@@ -313,13 +315,14 @@ __device__ bool nth_long(const LinearCall& c, int n, int64_t* seq)
     *seq = found;
     return n < 0;
 }
-__global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, const LinearScan s)
+__global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, const LinearScans scans, int parts)
 {
+    const LinearScan& s = scans.s[blockIdx.x / parts];
     __shared__ LinearItem first;
     __shared__ int64_t item0;
     const int h = blockIdx.y;
     int64_t seq = blockIdx.z;
-    const int hs = s.DK * s.DV, e0 = blockIdx.x * kPassElems + 4 * threadIdx.x;
+    const int hs = s.DK * s.DV, e0 = blockIdx.x % parts * kPassElems + 4 * threadIdx.x;
     linear_follow();
     if (c.cu_seqlens && !nth_long(c, blockIdx.z, &seq)) return;
     if (threadIdx.x == 0) {
@@ -595,28 +598,44 @@ cudaError_t launch_short(LinearShort p, int DK, int64_t b, bool follows, cudaStr
 
 }  // namespace
 
-cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, bool follows, cudaStream_t st)
+cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st)
 {
     if (c.items == 0) return cudaSuccess;
-    const auto run = [&](const LinearCall& call, bool state_only, bool after) {
-        if (c.act == SSD_BF16) launch_scan_dk<__nv_bfloat16>(call, s, state_only, after, st);
-        else launch_scan_dk<float>(call, s, state_only, after, st);
-        return cudaGetLastError();
-    };
-    if (!c.split) return run(c, false, follows);
-    cudaError_t e = run(c, true, follows);
-    if (e == cudaSuccess) e = launch_linear_pass(c, s, st);
-    LinearCall after = c;
-    after.clear_status = false;
-    return e == cudaSuccess ? run(after, false, true) : e;
+    LinearCall call = c;
+    bool follows = false, done[kMaxScans] = {};
+    for (int i = 0; i < nscans; ++i) {
+        if (done[i]) continue;
+        LinearScans s{};
+        for (int j = i; j < nscans; ++j) {
+            if (done[j] || scans[j].DK != scans[i].DK || scans[j].DV != scans[i].DV) continue;
+            done[j] = true;
+            s.s[s.n++] = scans[j];
+        }
+        const auto run = [&](bool state_only) {
+            if (c.act == SSD_BF16) launch_scan_dk<__nv_bfloat16>(call, s, state_only, follows, st);
+            else launch_scan_dk<float>(call, s, state_only, follows, st);
+            follows = true;
+            call.clear_status = false;
+            return cudaGetLastError();
+        };
+        cudaError_t e = cudaSuccess;
+        if (c.split) {
+            e = run(true);
+            if (e == cudaSuccess) e = launch_linear_pass(c, s, st);
+        }
+        if (e == cudaSuccess) e = run(false);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
-cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st)
+cudaError_t launch_linear_pass(const LinearCall& c, const LinearScans& scans, cudaStream_t st)
 {
     LaunchScope ls("linear_pass", st);
     const int64_t rows = c.cu_seqlens && c.T / c.seg_tokens < c.b ? c.T / c.seg_tokens : c.b;
-    return linear_launch(true, linear_pass_kernel, dim3((unsigned)((s.DK * s.DV + kPassElems - 1) / kPassElems), (unsigned)c.H, (unsigned)rows),
-                         256, 0, st, c, s);
+    const int parts = (scans.s[0].DK * scans.s[0].DV + kPassElems - 1) / kPassElems;
+    return linear_launch(true, linear_pass_kernel, dim3((unsigned)(parts * scans.n), (unsigned)c.H, (unsigned)rows), 256, 0, st, c,
+                         scans, parts);
 }
 
 // Splitting rows into segments fills SMs that whole rows would leave idle, at the price of a pass over
@@ -662,7 +681,7 @@ int64_t segment_tc(int64_t b, int64_t L, int64_t T, bool packed, int H, int nsca
 // scheduler, w times its issue slots (0.066 + 0.0004 dk; states half of it), and a little more where the two
 // are near: so segments are cut until the schedulers have some three warps each. A CTA's state comes and goes
 // at some 15 KB a us of its SM; the pass that joins the segments takes 0.07 a segment of a row.
-int64_t segment_simt(int64_t b, int64_t L, int64_t T, bool packed, int H, int DK, int DV, int sms)
+int64_t segment_simt(int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int DK, int DV, int sms)
 {
     const int64_t tiles = ((packed ? T : L) + kTile - 1) / kTile;
     if (tiles <= 1 || b == 0) return 2 * kTile;
@@ -681,7 +700,8 @@ int64_t segment_simt(int64_t b, int64_t L, int64_t T, bool packed, int H, int DK
         const int64_t share = (int64_t)((double)tiles * H / ctas) + 1;
         return (share > 4 ? share : 4) * kTile;
     }
-    const int64_t rows = b * H;
+    // the three scans of a backward pass run together where their shapes are one, else two and one
+    const int64_t rows = b * H * (nscans < 2 || DK == DV ? nscans : 2);
     double best = pass(rows, (double)tiles, 0.25, slots);    // whole rows
     int64_t best_seg = tiles + 1;
     for (int64_t nseg = 2; nseg <= tiles && nseg <= 512; ++nseg) {
@@ -701,7 +721,7 @@ int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool pac
                               int* sub)
 {
     *sub = 1;
-    return tc ? segment_tc(b, L, T, packed, H, nscans, sms, sub) : segment_simt(b, L, T, packed, H, DK, DV, sms);
+    return tc ? segment_tc(b, L, T, packed, H, nscans, sms, sub) : segment_simt(b, L, T, packed, H, nscans, DK, DV, sms);
 }
 
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,

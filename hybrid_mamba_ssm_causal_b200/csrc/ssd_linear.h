@@ -33,6 +33,13 @@ struct LinearScan {
     float* seg_states;   // workspace: [item][H][DV][DK], used when rows are split
 };
 
+// Scans of one shape, which run in the same launches.
+constexpr int kMaxScans = 3;
+struct LinearScans {
+    LinearScan s[kMaxScans];
+    int n;
+};
+
 // What the scans of one call share.
 struct LinearCall {
     int64_t b, L, T;     // sequences, tokens per row (fixed length), token rows in all
@@ -79,10 +86,10 @@ inline LinearCall linear_pieces(const LinearCall& c)
 bool linear_tc_supported(const LinearScan& s, int act);
 // nscans scans (1, or the 3 of a backward pass) in as few launches as the split allows.
 cudaError_t launch_linear_tc(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st);
-cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan& s, bool follows, cudaStream_t st);
+cudaError_t launch_linear_simt(const LinearCall& c, const LinearScan* scans, int nscans, cudaStream_t st);
 // The states entering every segment of rows that have more than one, from the pieces' own states; c as
 // linear_pieces gives it.
-cudaError_t launch_linear_pass(const LinearCall& c, const LinearScan& s, cudaStream_t st);   // follows a launch
+cudaError_t launch_linear_pass(const LinearCall& c, const LinearScans& scans, cudaStream_t st);   // follows a launch
 // (follows a launch)
 cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int64_t rows, int G, int r, int D, int act,
                                     cudaStream_t st);

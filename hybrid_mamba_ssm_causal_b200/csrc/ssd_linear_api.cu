@@ -67,9 +67,8 @@ void plan(ssd::LinearCall* c, const ssd_linear_dims* d, bool packed, int nscans)
     c->L = d->seqlen;
     c->H = d->nheads;
     c->act = d->act;
-    // on CUDA cores the scans of a backward pass run one after another
     c->seg_tokens = ssd::linear_segment_tokens(on_tensor_cores(d), d->batch, c->L, c->T, packed, d->nheads,
-                                               on_tensor_cores(d) ? nscans : 1, d->dk, d->dv, ssd::device_sm_count(), &c->sub);
+                                               nscans, d->dk, d->dv, ssd::device_sm_count(), &c->sub);
     if (packed) {
         c->nseg = 0;
         c->items = d->batch > 0 ? d->batch + c->T / c->seg_tokens : 0;
@@ -119,12 +118,7 @@ ssd_status run(const ssd::LinearCall& c, const ssd::LinearScan* s, int n, cudaSt
 {
     if (ssd::linear_tc_supported(s[0], c.act))
         return ssd::launch_linear_tc(c, s, n, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
-    ssd::LinearCall call = c;
-    for (int i = 0; i < n; ++i) {
-        if (ssd::launch_linear_simt(call, s[i], i > 0, st) != cudaSuccess) return SSD_ERR_CUDA;
-        call.clear_status = false;
-    }
-    return SSD_OK;
+    return ssd::launch_linear_simt(c, s, n, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 }  // namespace

@@ -96,7 +96,6 @@ static_assert(sizeof(Work) <= 1072, "room for two");
 struct ScanMaps {
     CUtensorMap q, k, v, o;
 };
-constexpr int kMaxScans = 3;
 struct TcArgs {
     LinearCall c;
     LinearScan s[kMaxScans];
@@ -880,7 +879,11 @@ cudaError_t launch_shape(const TcArgs& a, const TcMaps& m, bool follows, cudaStr
         TcArgs fine = a;
         fine.c = linear_pieces(a.c);
         cudaError_t e = launch_one<DK, DV, true>(fine, m, follows, st);
-        for (int i = 0; i < a.nscans && e == cudaSuccess; ++i) e = launch_linear_pass(fine.c, a.s[i], st);
+        if (e == cudaSuccess) {
+            LinearScans all{};
+            for (int i = 0; i < a.nscans; ++i) all.s[all.n++] = a.s[i];
+            e = launch_linear_pass(fine.c, all, st);
+        }
         if (e != cudaSuccess) return e;
         TcArgs after = a;
         after.c.clear_status = false;
