@@ -18,6 +18,7 @@
 #include "../../include/ssd_mixer.h"
 #include "ssd_common.cuh"
 #include "ssd_layer_norm.h"
+#include "ssd_pdl.cuh"
 #include "ssd_profile.h"
 
 namespace ssd {
@@ -161,6 +162,16 @@ __device__ __forceinline__ void load_params(const float* p, int64_t c, float non
     }
 }
 
+// N floats from an address that 4 N bytes (at most 16) divide: one by one, a warp's stores would touch each
+// sector several times (256 blocks of 2 x 2688: 12.8 us for the call, in vectors 6.8).
+template <int N>
+__device__ __forceinline__ void store_params(float* p, const float* v)
+{
+    if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
 // Sum over a team of TEAM lanes, or (TEAM = 0) over the block, in a fixed order. One barrier a call,
 // so successive calls take different `red` (32 values).
 template <int TEAM>
@@ -443,16 +454,15 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) layer_norm_grad_kernel(c
         dx += it.stride * p.y_ld;
     }
     copy_wait<0>();
+    pdl_release();
     if (!p.part) return;
     float* part = p.part + (int64_t)blockIdx.y * 2 * C;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (it.in(i))
-#pragma unroll
-            for (int e = 0; e < V::kN; ++e) {
-                part[it.col(i) + e] = dw[i][e];
-                part[C + it.col(i) + e] = db[i][e];
-            }
+        if (it.in(i)) {
+            store_params<V::kN>(part + it.col(i), dw[i]);
+            store_params<V::kN>(part + C + it.col(i), db[i]);
+        }
 }
 
 // Sums of the partial sums, 32 channels a block, its 8 warps sharing the parts: each in order, then
@@ -462,6 +472,7 @@ __global__ void __launch_bounds__(256) layer_norm_parts_kernel(const LayerNorm p
     __shared__ float s[8][32];
     const int64_t C = p.channels(), c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const int warp = threadIdx.x >> 5;
+    pdl_wait();
     float a = 0.0f;
     if (c < C)
 #pragma unroll 8
@@ -618,15 +629,19 @@ cudaError_t backward(const LayerNorm& p, int parts, cudaStream_t st)
             layer_norm_dw_kernel<T><<<dim3((unsigned)((p.channels() + 255) / 256), (unsigned)parts), 256, 0, st>>>(p, parts);
         }
         LaunchScope ls("layer_norm_parts", st);
-        layer_norm_parts_kernel<<<dim3((unsigned)((p.channels() + 31) / 32), 2), 256, 0, st>>>(p, parts);
+        const cudaError_t e = pdl_launch(true, layer_norm_parts_kernel, dim3((unsigned)((p.channels() + 31) / 32), 2), 256, 0,
+                                         st, p, parts);
+        if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
 }
 
 }  // namespace
 
-// Rows a backward pass works on at a time: as many blocks as are resident on the device. The vector's
-// width follows from addresses that are not known here, so the larger of the two counts is kept.
+// Rows a backward pass works on at a time: as many blocks as are resident on the device, but no fewer than
+// four rows to each (its partial sums cost as much as some rows; 256 x 2688 bf16 6.2 us, one row each 6.8;
+// 512 x 32 groups of 128 6.5 and 9.4) unless that leaves fewer than 64. The vector's width follows from
+// addresses that are not known here, so the larger of the two counts is kept.
 int layer_norm_parts(int64_t rows, int groups, int width, int act, int sms)
 {
     int64_t parts = 64;
@@ -638,7 +653,8 @@ int layer_norm_parts(int64_t rows, int groups, int width, int act, int sms)
         const int64_t fit = rows_at_a_time(s, sms);
         parts = parts > fit ? parts : fit;
     }
-    return (int)(rows < 1 ? 1 : (rows < parts ? rows : parts));
+    const int64_t four = (rows + 3) / 4, few = four > 64 ? four : (rows < 64 ? rows : 64);
+    return (int)(few < 1 ? 1 : (few < parts ? few : parts));
 }
 
 cudaError_t launch_layer_norm(const LayerNorm& p, cudaStream_t st)

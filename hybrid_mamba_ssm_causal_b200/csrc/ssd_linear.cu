@@ -8,6 +8,7 @@
 #include "../../include/ssd_mixer.h"
 #include "ssd_common.cuh"
 #include "ssd_linear.h"
+#include "ssd_pdl.cuh"
 #include "ssd_profile.h"
 #include "ssd_tc_util.cuh"
 
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     constexpr int kPer = (kTileVecs + kThr - 1) / kThr;
     __shared__ __align__(16) T s_in[kTile][2 * DK + DV];      // k, then q, then v
     __shared__ __align__(16) float s_o[kTile][DV];
-    linear_wait();
+    pdl_wait();
     if (c.clear_status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *c.status = kDevOk;
 
     const int h = blockIdx.x % c.H;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
             }
         }
     }
-    linear_release();      // not earlier: a successor's blocks, placed beside unfinished ones, crowd some SMs (42 -> 37 us)
+    pdl_release();      // not earlier: a successor's blocks, placed beside unfinished ones, crowd some SMs (42 -> 37 us)
     if (s.reverse && it.n > 0) {
 #pragma unroll
         for (int r = 0; r < kPairs; ++r)
@@ -260,7 +261,7 @@ void launch_scan_shape(const LinearCall& c, const LinearScans& s, bool state_onl
 {
     constexpr int kWarps = DV / SimtShape<DK>::kWarpRows > 0 ? DV / SimtShape<DK>::kWarpRows : 1;
     LaunchScope ls(state_only ? "linear_states" : "linear_scan", st);
-    linear_launch(follows, linear_scan_kernel<T, DK, DV>, dim3((unsigned)(c.items * c.H), (unsigned)s.n), 32 * kWarps, 0,
+    pdl_launch(follows, linear_scan_kernel<T, DK, DV>, dim3((unsigned)(c.items * c.H), (unsigned)s.n), 32 * kWarps, 0,
                   st, c, s, state_only);
 }
 template <typename T, int DK>
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
     const int h = blockIdx.y;
     int64_t seq = blockIdx.z;
     const int hs = s.DK * s.DV, e0 = blockIdx.x % parts * kPassElems + 4 * threadIdx.x;
-    linear_follow();
+    pdl_follow();
     if (c.cu_seqlens && !nth_long(c, blockIdx.z, &seq)) return;
     if (threadIdx.x == 0) {
         item0 = c.cu_seqlens ? linear_packed_first(c, seq) : seq * c.nseg;
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(256) linear_group_sum_kernel(const float* __re
                                                                int64_t n, int G, int r, int D)
 {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    linear_follow();
+    pdl_follow();
     if (i >= n) return;
     const int64_t w = (int64_t)G * D, row = i / w;
     const int col = (int)(i - row * w), g = col / D, d = col - g * D;
@@ -401,7 +402,7 @@ constexpr int kListThreads = 1024, kBuckets = 256;
 __global__ void __launch_bounds__(kListThreads) linear_list_kernel(const LinearCall c)
 {
     __shared__ int start[2][kBuckets];
-    linear_follow();
+    pdl_follow();
     if (threadIdx.x < 64) c.status[threadIdx.x] = 0;          // the status word, the counts, what is taken
     for (int i = threadIdx.x; i < 2 * kBuckets; i += kListThreads) (&start[0][0])[i] = 0;
     __syncthreads();
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kShortThreads) linear_short_kernel(const Linea
     constexpr int kTokens = ONE ? 1 : kLinearShort;
     const int64_t seq = blockIdx.y;
     const int h = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
-    if (!ONE) linear_follow();
+    if (!ONE) pdl_follow();
     if (!ONE && p.status && blockIdx.x == 0 && seq == 0 && threadIdx.x == 0) *p.status = kDevOk;
     int64_t row = seq * p.L, n = p.L;
     if (!ONE && p.cu_seqlens) {
@@ -589,10 +590,10 @@ cudaError_t launch_short(LinearShort p, int DK, int64_t b, bool follows, cudaStr
     LaunchScope ls(ONE ? "linear_decode" : "linear_short", st);
     const dim3 grid((unsigned)(p.H * p.parts), (unsigned)b);
     switch (DK) {
-    case 16: return linear_launch(follows, linear_short_kernel<T, 16, ONE>, grid, kShortThreads, 0, st, p);
-    case 32: return linear_launch(follows, linear_short_kernel<T, 32, ONE>, grid, kShortThreads, 0, st, p);
-    case 64: return linear_launch(follows, linear_short_kernel<T, 64, ONE>, grid, kShortThreads, 0, st, p);
-    default: return linear_launch(follows, linear_short_kernel<T, 128, ONE>, grid, kShortThreads, 0, st, p);
+    case 16: return pdl_launch(follows, linear_short_kernel<T, 16, ONE>, grid, kShortThreads, 0, st, p);
+    case 32: return pdl_launch(follows, linear_short_kernel<T, 32, ONE>, grid, kShortThreads, 0, st, p);
+    case 64: return pdl_launch(follows, linear_short_kernel<T, 64, ONE>, grid, kShortThreads, 0, st, p);
+    default: return pdl_launch(follows, linear_short_kernel<T, 128, ONE>, grid, kShortThreads, 0, st, p);
     }
 }
 
@@ -634,7 +635,7 @@ cudaError_t launch_linear_pass(const LinearCall& c, const LinearScans& scans, cu
     LaunchScope ls("linear_pass", st);
     const int64_t rows = c.cu_seqlens && c.T / c.seg_tokens < c.b ? c.T / c.seg_tokens : c.b;
     const int parts = (scans.s[0].DK * scans.s[0].DV + kPassElems - 1) / kPassElems;
-    return linear_launch(true, linear_pass_kernel, dim3((unsigned)(parts * scans.n), (unsigned)c.H, (unsigned)rows), 256, 0, st, c,
+    return pdl_launch(true, linear_pass_kernel, dim3((unsigned)(parts * scans.n), (unsigned)c.H, (unsigned)rows), 256, 0, st, c,
                          scans, parts);
 }
 
@@ -731,8 +732,8 @@ cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int6
     if (n == 0) return cudaSuccess;
     LaunchScope ls("linear_group_sum", st);
     const unsigned grid = (unsigned)((n / 4 + 255) / 256);
-    return act == SSD_BF16 ? linear_launch(true, linear_group_sum_kernel<__nv_bfloat16>, dim3(grid), 256, 0, st, in, (__nv_bfloat16*)out, ld, n, G, r, D)
-                           : linear_launch(true, linear_group_sum_kernel<float>, dim3(grid), 256, 0, st, in, (float*)out, ld, n, G, r, D);
+    return act == SSD_BF16 ? pdl_launch(true, linear_group_sum_kernel<__nv_bfloat16>, dim3(grid), 256, 0, st, in, (__nv_bfloat16*)out, ld, n, G, r, D)
+                           : pdl_launch(true, linear_group_sum_kernel<float>, dim3(grid), 256, 0, st, in, (float*)out, ld, n, G, r, D);
 }
 
 cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st)

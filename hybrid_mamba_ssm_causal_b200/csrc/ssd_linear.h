@@ -106,33 +106,6 @@ int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool pac
 
 #ifdef __CUDACC__
 
-// A call's kernels follow one another by programmatic dependent launch: each lets its successor start
-// (blocks placed, shared and tensor memory set up) as it starts itself, and waits for its predecessor
-// before it touches global memory (the scan on CUDA cores lets it start later). Every block waits, so that
-// a kernel's end implies its predecessor's. A call's first kernel is launched plainly.
-__device__ __forceinline__ void linear_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void linear_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void linear_follow()
-{
-    linear_release();
-    linear_wait();
-}
-template <typename... P, typename... A>
-cudaError_t linear_launch(bool follows, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = follows ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // lambda = exp(log_decay): -inf (no memory) is taken as exp(-1e4) = 0 so that 0 * log_decay is 0.
 __device__ __forceinline__ float linear_log_decay(const float* log_decay, int h) { return fmaxf(log_decay[h], -1e4f); }
 

@@ -47,6 +47,7 @@
 #include "../../include/ssd_mixer.h"
 #include "ssd_common.cuh"
 #include "ssd_linear.h"
+#include "ssd_pdl.cuh"
 #include "ssd_profile.h"
 #include "ssd_tc_util.cuh"
 
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the compiler sees
     const uint32_t sb = smem_u32(smem);
     if (sb & 1023u) {
-        linear_follow();
+        pdl_follow();
         if (c.clear_status && blockIdx.x == 0 && tid == 0) *c.status = kDevOk;
         if (tid == 0) set_device_status(c.status, kDevSmemMisaligned);
         return;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    linear_follow();
+    pdl_follow();
     if (c.clear_status && blockIdx.x == 0 && tid == 0) *c.status = kDevOk;
     // segments of this launch, of every head and scan
     const int64_t total = (c.list ? (int64_t)c.counts[STATES ? 1 : 0] : c.items) * c.H * a.nscans;
@@ -869,7 +870,7 @@ cudaError_t launch_one(const TcArgs& a, const TcMaps& m, bool follows, cudaStrea
     if (e != cudaSuccess) return e;
     LaunchScope ls(STATES ? "linear_tc_states" : "linear_tc", st);
     const int64_t total = a.c.items * a.c.H * a.nscans, sms = device_sm_count();
-    return linear_launch(follows, linear_tc_kernel<DK, DV, STATES>, dim3((unsigned)(total < sms ? total : sms)), kThreads, C::kSmem, st, a, m);
+    return pdl_launch(follows, linear_tc_kernel<DK, DV, STATES>, dim3((unsigned)(total < sms ? total : sms)), kThreads, C::kSmem, st, a, m);
 }
 
 template <int DK, int DV>
