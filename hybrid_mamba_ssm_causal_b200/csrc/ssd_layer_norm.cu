@@ -9,7 +9,8 @@
 // instructions in practice: few operations an element and few shuffles a row decide. A thread holds NV
 // vectors of 16 (or, for rows that only 8 divides, 8) bytes of a row; a group is summed by a team,
 // either a power of two of lanes of one warp (head norms: no barrier at all) or the whole block.
-// Rows that are not so aligned, and teams that would not fit, take a loop of one warp per (row, group).
+// Rows that are not so aligned are read element by element, forwards into registers too; teams that would
+// not fit, and gradients of such rows, take a loop of one warp per (row, group).
 //   Forwards, block teams: a block per row, many on an SM, so that one's barriers are the others' time.
 //   All others walk down the rows on one set of columns, the coming rows on their way into shared
 //   memory, where each thread copies and reads its own vectors only: several rows in flight without a
@@ -100,16 +101,18 @@ __global__ void __launch_bounds__(256) layer_norm_dw_kernel(const LayerNorm p, i
 }
 
 // ------------------------------------------------------------------ vectors
-// VB bytes of a row: the raw words, and how many elements they are.
+// VB bytes of a row (16, 8, or a single element): the raw words, and how many elements they are.
 template <typename T, int VB>
 struct RowVec {
-    static constexpr int kN = VB / (int)sizeof(T), kW = VB / 4;   // elements, words
+    static constexpr int kN = VB / (int)sizeof(T), kW = VB < 4 ? 1 : VB / 4;   // elements, words
     uint32_t w[kW];
     __device__ __forceinline__ void load(const T* p)
     {
         if constexpr (VB == 16) {
             const uint4 v = *reinterpret_cast<const uint4*>(p);
             w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (kN == 1) {
+            w[0] = __float_as_uint(ld_f(p));
         } else {
             const uint2 v = *reinterpret_cast<const uint2*>(p);
             w[0] = v.x; w[1] = v.y;
@@ -122,14 +125,14 @@ struct RowVec {
     }
     __device__ __forceinline__ float at(int i) const
     {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        if constexpr (sizeof(T) == 4 || kN == 1) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
     __device__ __forceinline__ void set(const float* f)
     {
 #pragma unroll
         for (int i = 0; i < kW; ++i) {
-            if constexpr (sizeof(T) == 4) {
+            if constexpr (sizeof(T) == 4 || kN == 1) {
                 w[i] = __float_as_uint(f[i]);
             } else {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
@@ -140,6 +143,7 @@ struct RowVec {
     __device__ __forceinline__ void store(T* p) const
     {
         if constexpr (VB == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (kN == 1) *p = Act<T>::from_f(__uint_as_float(w[0]));
         else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
 };
@@ -150,6 +154,8 @@ __device__ __forceinline__ void load_params(const float* p, int64_t c, float non
     if (!p) {
 #pragma unroll
         for (int i = 0; i < N; ++i) f[i] = none;
+    } else if constexpr (N == 1) {
+        f[0] = p[c];
     } else if constexpr (N == 2) {
         const float2 v = *reinterpret_cast<const float2*>(p + c);
         f[0] = v.x; f[1] = v.y;
@@ -546,19 +552,21 @@ template <typename T, int VB>
 bool forward_vec(const LayerNorm& p, cudaStream_t st, cudaError_t* e)
 {
     const int vecs = p.width / RowVec<T, VB>::kN;
-    if (lane_team(vecs)) {
-        const RowShape s = row_shape(p.groups, p.width, RowVec<T, VB>::kN);
-        int64_t rows = rows_at_a_time(s, device_sm_count());
-        rows = rows < p.rows ? rows : p.rows;
-        const auto go = [&](auto kernel) { *e = launch_rows(kernel, p, s, 1, VB, rows < 65535 ? rows : 65535, st); };
-        switch (vecs) {
-        case 2: go(layer_norm_lanes_kernel<T, VB, 2>); break;
-        case 4: go(layer_norm_lanes_kernel<T, VB, 4>); break;
-        case 8: go(layer_norm_lanes_kernel<T, VB, 8>); break;
-        case 16: go(layer_norm_lanes_kernel<T, VB, 16>); break;
-        default: go(layer_norm_lanes_kernel<T, VB, 32>); break;
+    if constexpr (RowVec<T, VB>::kN > 1) {
+        if (lane_team(vecs)) {
+            const RowShape s = row_shape(p.groups, p.width, RowVec<T, VB>::kN);
+            int64_t rows = rows_at_a_time(s, device_sm_count());
+            rows = rows < p.rows ? rows : p.rows;
+            const auto go = [&](auto kernel) { *e = launch_rows(kernel, p, s, 1, VB, rows < 65535 ? rows : 65535, st); };
+            switch (vecs) {
+            case 2: go(layer_norm_lanes_kernel<T, VB, 2>); break;
+            case 4: go(layer_norm_lanes_kernel<T, VB, 4>); break;
+            case 8: go(layer_norm_lanes_kernel<T, VB, 8>); break;
+            case 16: go(layer_norm_lanes_kernel<T, VB, 16>); break;
+            default: go(layer_norm_lanes_kernel<T, VB, 32>); break;
+            }
+            return true;
         }
-        return true;
     }
     const unsigned grid = (unsigned)(p.rows * p.groups), warps = (unsigned)((p.rows * p.groups + 3) / 4);
     // Rows of up to 384 vectors: a warp each (58 against 80 us for 65536 x 1024 bf16, 89 against 109 for
@@ -603,7 +611,7 @@ cudaError_t forward(const LayerNorm& p, cudaStream_t st)
     LaunchScope ls("layer_norm", st);
     const int vb = vector_bytes<T>(p);
     cudaError_t e = cudaSuccess;
-    if (vb == 16 ? forward_vec<T, 16>(p, st, &e) : vb == 8 && forward_vec<T, 8>(p, st, &e)) return e;
+    if (vb == 16 ? forward_vec<T, 16>(p, st, &e) : vb == 8 ? forward_vec<T, 8>(p, st, &e) : forward_vec<T, sizeof(T)>(p, st, &e)) return e;
     const int64_t segs = p.rows * p.groups;
     layer_norm_kernel<T><<<(unsigned)((segs + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(p);
     return cudaGetLastError();
