@@ -39,7 +39,7 @@ struct SimtShape {
     static constexpr int kWarpRows = kRows * (32 / kLanes);
 };
 
-// N neighbouring values of a row in shared memory, aligned to their own size
+// N neighbouring values of a row, aligned to their own size
 template <int N>
 __device__ __forceinline__ void load_row(const float* p, float* out)
 {
@@ -77,6 +77,20 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float* out)
         out[2 * i] = __uint_as_float(w[i] << 16);
         out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v)
+{
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+template <int N>
+__device__ __forceinline__ void store_row(float* p, const float* v)
+{
+    if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else *p = v[0];
 }
 
 template <typename T, int DK, int DV>
@@ -117,19 +131,31 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     for (int r = 0; r < kPairs; ++r)
 #pragma unroll
         for (int e = 0; e < Sh::kCols; ++e) S[r][e] = splat2(0.0f);
+    const auto load_state = [&](const float* p) {    // [DV][DK]
+#pragma unroll
+        for (int r = 0; r < kPairs; ++r) {
+            float x[Sh::kCols], y[Sh::kCols];
+            load_row<Sh::kCols>(p + (d0 + 2 * r) * DK + e0, x);
+            load_row<Sh::kCols>(p + (d0 + 2 * r + 1) * DK + e0, y);
+#pragma unroll
+            for (int e = 0; e < Sh::kCols; ++e) S[r][e] = make_float2(x[e], y[e]);
+        }
+    };
     if (!state_only) {
         if (it.nseg > 1) {   // never the slot itself: the row's last segment may be rewriting it
-            const float* p = s.seg_states + (item * c.H + h) * hs;
-#pragma unroll
-            for (int r = 0; r < kPairs; ++r)
-#pragma unroll
-                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = make_float2(p[(d0 + 2 * r) * DK + e0 + e], p[(d0 + 2 * r + 1) * DK + e0 + e]);
+            load_state(s.seg_states + (item * c.H + h) * hs);
         } else if (linear_has_init(c, s, it.seq)) {
             const float* p = s.init + (it.slot * c.H + h) * hs;
+            if (s.init_cs == 1) {
+                load_state(p);                       // rows of DK
+            } else {
 #pragma unroll
-            for (int r = 0; r < kPairs; ++r)
+                for (int r = 0; r < kPairs; ++r)
 #pragma unroll
-                for (int e = 0; e < Sh::kCols; ++e) S[r][e] = make_float2(p[(d0 + 2 * r) * s.init_rs + (e0 + e) * s.init_cs], p[(d0 + 2 * r + 1) * s.init_rs + (e0 + e) * s.init_cs]);
+                    for (int e = 0; e < Sh::kCols; ++e)
+                        S[r][e] = make_float2(p[(d0 + 2 * r) * s.init_rs + (e0 + e) * s.init_cs],
+                                              p[(d0 + 2 * r + 1) * s.init_rs + (e0 + e) * s.init_cs]);
+            }
         }
     }
 
@@ -227,11 +253,12 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
         else walk(std::false_type{});
         if (!state_only) {
             __syncthreads();
-            for (int id = tid; id < nt * DV; id += kThr) {
-                const int tt = id / DV, d = id % DV;
+            for (int id = tid; id < nt * (DV / 4); id += kThr) {
+                const int tt = id / (DV / 4), d = id % (DV / 4) * 4;
                 const int64_t at = (it.row0 + t0 + tt) * s.o_ld + (int64_t)h * DV + d;
-                if (s.o_f32) ((float*)s.o)[at] = s_o[tt][d];
-                else ((T*)s.o)[at] = Act<T>::from_f(s_o[tt][d]);
+                const float4 y = *reinterpret_cast<const float4*>(&s_o[tt][d]);
+                if (s.o_f32) *reinterpret_cast<float4*>((float*)s.o + at) = y;
+                else store4((T*)s.o + at, y);
             }
         }
     }
@@ -247,12 +274,16 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     else if (last && s.final_state) out = s.final_state + (it.slot * c.H + h) * hs;
     if (out) {
 #pragma unroll
-        for (int r = 0; r < kPairs; ++r)
+        for (int r = 0; r < kPairs; ++r) {
+            float x[Sh::kCols], y[Sh::kCols];
 #pragma unroll
             for (int e = 0; e < Sh::kCols; ++e) {
-                out[(d0 + 2 * r) * DK + e0 + e] = S[r][e].x;
-                out[(d0 + 2 * r + 1) * DK + e0 + e] = S[r][e].y;
+                x[e] = S[r][e].x;
+                y[e] = S[r][e].y;
             }
+            store_row<Sh::kCols>(out + (d0 + 2 * r) * DK + e0, x);
+            store_row<Sh::kCols>(out + (d0 + 2 * r + 1) * DK + e0, y);
+        }
     }
 }
 
@@ -390,8 +421,7 @@ __global__ void __launch_bounds__(256) linear_group_sum_kernel(const float* __re
         const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)k * D);
         a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
     }
-    T* o = out + row * ld + col;
-    o[0] = Act<T>::from_f(a.x); o[1] = Act<T>::from_f(a.y); o[2] = Act<T>::from_f(a.z); o[3] = Act<T>::from_f(a.w);
+    store4(out + row * ld + col, a);
 }
 
 // ------------------------------------------------------------------- lists of segments
