@@ -147,7 +147,9 @@ struct RowVec {
         else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
 };
-// N parameters from column c (aligned to 4 N bytes, at most 16), or a constant.
+// N parameters from column c (aligned to 4 N bytes), or a constant. Eight come as one load of 32 bytes a lane:
+// as two of 16 a warp's loads would pass through the L1 with gaps, at half its rate, which is what bound wide
+// rows of bf16 (16384 x 8192: 127 us, now 104).
 template <int N>
 __device__ __forceinline__ void load_params(const float* p, int64_t c, float none, float* f)
 {
@@ -159,12 +161,14 @@ __device__ __forceinline__ void load_params(const float* p, int64_t c, float non
     } else if constexpr (N == 2) {
         const float2 v = *reinterpret_cast<const float2*>(p + c);
         f[0] = v.x; f[1] = v.y;
+    } else if constexpr (N == 8) {
+        asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+            : "l"(p + c));
     } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p + c + i);
-            f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
-        }
+        static_assert(N == 4, "");
+        const float4 v = *reinterpret_cast<const float4*>(p + c);
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
     }
 }
 
@@ -500,7 +504,7 @@ int vector_bytes(const LayerNorm& p)
 {
     for (int vb = 16; vb >= 8; vb -= 8) {
         const int n = vb / (int)sizeof(T);
-        const uintptr_t par = n * 4 < 16 ? n * 4 : 16;
+        const uintptr_t par = n * 4;
         if (p.width % n || (uintptr_t)p.x % vb || (uintptr_t)p.y % vb || (uintptr_t)p.dy % vb || p.x_ld % n || p.y_ld % n ||
             p.dy_ld % n || (uintptr_t)p.weight % par || (uintptr_t)p.bias % par)
             continue;
@@ -569,17 +573,20 @@ bool forward_vec(const LayerNorm& p, cudaStream_t st, cudaError_t* e)
         }
     }
     const unsigned grid = (unsigned)(p.rows * p.groups), warps = (unsigned)((p.rows * p.groups + 3) / 4);
-    // Rows of up to 384 vectors: a warp each (58 against 80 us for 65536 x 1024 bf16, 89 against 109 for
-    // 32768 x 2688), but a block where there are too few of them to fill the device (9 against 11 us for
-    // 256 x 2688). Blocks hold 32 elements a thread: fewer, or the parameters beside them, was slower
-    // (16384 x 8192 bf16: 127 us, with 16 elements 183), more too (132).
-    constexpr int kNV = RowVec<T, VB>::kN >= 8 ? 4 : 8;
-    if (vecs <= 384 && p.rows * p.groups >= (int64_t)device_sm_count() * 8) {
+    // Rows of up to 256 vectors of eight elements, or 384 smaller ones: a warp each (51 against 54 us for
+    // 65536 x 1024 bf16, 28 against 51 for 4096 x 12 groups of 333; 32768 x 2688 bf16, 336 vectors, 79
+    // against 75), but a block where there are too few of them to fill the device (8.8 against
+    // 11 us for 1200 x 1024). Blocks hold 32 elements a thread (16384 x 8192 bf16 104 us, 5.1 TB/s; x 4096
+    // 54, with half of that 76), with few rows half of that.
+    constexpr bool kEights = RowVec<T, VB>::kN >= 8;
+    constexpr int kNV = kEights ? 4 : 8;
+    const bool many = p.rows * p.groups >= (int64_t)device_sm_count() * 8;
+    if (many && vecs <= (kEights ? 256 : 384)) {
         if (vecs <= 64) layer_norm_block_kernel<T, VB, 2, 32><<<warps, 128, 0, st>>>(p);
         else if (vecs <= 128) layer_norm_block_kernel<T, VB, 4, 32><<<warps, 128, 0, st>>>(p);
-        else if (vecs <= 256) layer_norm_block_kernel<T, VB, 8, 32><<<warps, 128, 0, st>>>(p);
-        else layer_norm_block_kernel<T, VB, 12, 32><<<warps, 128, 0, st>>>(p);
-    } else if (vecs <= 512) layer_norm_block_kernel<T, VB, 2, 0><<<grid, round32((vecs + 1) / 2), 0, st>>>(p);
+        else if (kEights || vecs <= 256) layer_norm_block_kernel<T, VB, 8, 32><<<warps, 128, 0, st>>>(p);
+        else layer_norm_block_kernel<T, VB, kEights ? 8 : 12, 32><<<warps, 128, 0, st>>>(p);
+    } else if (!many && vecs <= 512) layer_norm_block_kernel<T, VB, 2, 0><<<grid, round32((vecs + 1) / 2), 0, st>>>(p);
     else if (vecs <= 4096) layer_norm_block_kernel<T, VB, kNV, 0><<<grid, round32((vecs + kNV - 1) / kNV), 0, st>>>(p);
     else return false;
     *e = cudaGetLastError();
