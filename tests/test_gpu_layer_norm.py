@@ -122,6 +122,21 @@ def test_backward(lead, groups, width, act):
     check_gradients(x, dy, None, mean, rstd, groups, *sm.layer_norm_backward(dy, x, None, mean, rstd, groups=groups))
 
 
+@pytest.mark.parametrize("offset", [1, 2, 4, 8])
+@pytest.mark.parametrize("lead,groups,width", [((3,), 1, 2688), ((1300,), 1, 1024), ((7,), 4, 128), ((2,), 1, 16384)])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_parameters_at_any_float(lead, groups, width, act, offset):
+    """weight and bias as slices of longer vectors, from one float's alignment to a vector's."""
+    x, dy, w, b = make(lead, groups, width, act, seed=offset)
+    C = groups * width
+    ws, bs = torch.zeros(C + 8, device="cuda"), torch.zeros(C + 8, device="cuda")
+    ws[offset:offset + C], bs[offset:offset + C] = w, b
+    w, b = ws[offset:offset + C], bs[offset:offset + C]
+    y, mean, rstd = sm.layer_norm(x, w, b, groups=groups)
+    check_norm(x, w, b, groups, 1e-5, y, mean, rstd)
+    check_gradients(x, dy, w, mean, rstd, groups, *sm.layer_norm_backward(dy, x, w, mean, rstd, groups=groups))
+
+
 def test_gradient_against_fp64_autograd_and_bits():
     x, dy, w, b = make((64,), 2, 96, "f32", seed=5)
     y, mean, rstd = sm.layer_norm(x, w, b, groups=2)
