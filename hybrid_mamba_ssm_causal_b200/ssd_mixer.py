@@ -706,7 +706,7 @@ def _workspace(ws, size: int, what: str, dev):
     if ws is None:
         if size == 0:
             raise SsdError(SSD_ERR_UNSUPPORTED, f"{what}: invalid or unsupported dims")
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        ws = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=dev)   # less host time than torch.empty
     elif not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -796,8 +796,9 @@ def linear_decode_step(dims: LinearDims, q, k, v, log_decay, state, slot_idx=Non
     ps = _whole(state, "state", (nslots, H, dims.dv, dims.dk), torch.float32, dev)
     with _On(dev, stream) as on:
         if o is None:
-            o = q.new_empty((b, H * dims.dv))
-            po = o.data_ptr(), H * dims.dv
+            w = H * dims.dv
+            o = torch.empty_strided((b, w), (w, 1), dtype=q.dtype, device=dev)
+            po = o.data_ptr(), w
         else:
             po = _rows_on(o, "o", b, H * dims.dv, dims.torch_dtype, dev)
         st = load_library().ssd_mixer_linear_decode_step(ctypes.byref(cd), *rows, pd, ps, nslots, psl, *po, on)
