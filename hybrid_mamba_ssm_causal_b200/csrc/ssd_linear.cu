@@ -674,13 +674,13 @@ cudaError_t launch_linear_pass(const LinearCall& c, const LinearScans& scans, cu
 // Splitting rows into segments fills SMs that whole rows would leave idle, at the price of a pass over
 // k and v before the main one and of the segments' states.
 namespace {
-// Tensor cores, in units of one block of 128 tokens of the main pass (some 3.3 us for 128 x 128): a CTA
-// per SM takes segment after segment, each some 1.8 to start and to end; a block of the states' pass is
-// 0.5; the two more launches 2, and every segment's state goes through memory four times.
+// Tensor cores, in units of one block of 128 tokens of the main pass (some 3.8 us for 128 x 128): a CTA
+// per SM takes segment after segment, each some 1.6 to start and to end; a block of the states' pass is
+// 0.5; the two more launches 1.8, and every segment's state goes through memory four times.
 int64_t segment_tc(int64_t b, int64_t L, int64_t T, bool packed, int H, int nscans, int sms, int* sub)
 {
     const int64_t rows = b * H * nscans;
-    const double start = 1.8, states = 0.58, join = 2.0, each = 0.01;
+    const double start = 1.6, states = 0.5, join = 1.8, each = 0.009;
     const int64_t blocks = ((packed ? T : L) + 127) / 128;
     if (blocks <= 1 || b == 0) return 256;                 // nothing to split: longer than any row
     if (packed && b > 1) {

@@ -8,12 +8,14 @@
 // (backwards the entering state has had its decay already: l^i S q_i, and l^n S + sum l^{n-j} u v_j k_j^T
 // leaves, decayed for the next block). Four products a block, all M = 128:
 //   QK     [i][j]  = Q K^T                       A, B: the TMA tiles, K-major
-//   inter  [i][d]  = Q S^T                       B: S in bf16, written by the state warps
+//   inter  [i][d]  = Q S^T                       B: S in two bf16 terms, written by the state warps
 //   U      [d][e]  = (w V)^T K                   A: w V transposed, in TMEM; B: the K tile, MN-major
 //   intra  [i][d]  = P V                         A: the decayed scores P in TMEM; B: the V tile, MN-major
 // S stays in fp32 registers, S = l^n S + U, and w V is taken as the sum of three bf16 (24 bits), so
-// that the state is as exact as its fp32 sums; P and the operand copy of S are rounded to bf16 once,
-// which is as much as the rounding of o itself.
+// that the state is as exact as its fp32 sums. P and the operand copy of S are sums of two bf16 (16
+// bits): o is rounded once, when it is stored. With one term each, o's error against 64 bits was 1.4
+// times that of its rounding (rms 2.35e-3 of the values, now 1.66e-3); the second costs a third more matrix
+// instructions (1 x 2048 x 148 heads of 128 69 -> 82 us).
 //
 // One CTA per SM, which takes segment after segment; a row that is cut into several has their own
 // states computed first (the same kernel without q and o) and joined by a small kernel between.
@@ -22,21 +24,22 @@
 // tile in them (setmaxnreg):
 //   0    outputs, a row i each: scores -> P; inter times c l^{i+1}, in place, for intra to add to; then
 //        o, staged over the block's own tiles for a TMA store
-//   1    state, a row d each: S += U, and its operand copy
+//   1    state, a row d each: S += U, and its operand copy, 32 columns at a time in two slots in turn
 //   2, 3 w V: V's tile transposed by ldmatrix, times w, into TMEM, 32 tokens at a time in a slot each
 //   4    a warp for the list of segments (where each lies and its head's powers of l, one segment ahead)
 //        and their TMA loads, one for the stores, one for the MMAs of the outputs and one for those of the
 //        state, which would otherwise wait for one another
-// TMEM columns: QK and, over its first half, P; one output tile; U; the two slots of w V. The loops are
+// TMEM columns: QK and, in its place, both terms of P; one output tile; U; the two slots of w V. The loops are
 // kept rolled where registers allow: the warpgroups' code competes for the instruction cache (scores
 // unrolled by four: 106 us where 72 are). Nothing may spill: beside 227 KB of shared memory the L1 has some
 // 16 KB left, and a reload waits behind the tiles.
 //
-// Measured: 1 x 2048 tokens x 148 heads of 128, a row per SM, 69 us (4.8 TB/s of operands; tensor pipe
-// 47 % busy, issue slots 53 %, DRAM 52 %): 3.9 us a block, of which 1.7 are matrix instructions and 2.5
-// HBM. With few rows the chain of one block bounds it, 3.3-3.5 us (2.2 for 64 x 64), and a segment's start
-// and end, some 6. Tried: P in columns of its own with w V in slots of 16 tokens, the next block's QK
-// before this one's intra (82 us); scores and outputs on two warpgroups, w V on one (82).
+// Measured: 1 x 2048 tokens x 148 heads of 128, a row per SM, 82 us (4.0 TB/s of operands): 5.1 us a block,
+// of which 2.3 are matrix instructions and 2.5 HBM. With few rows the chain of one block bounds it, 3.8-3.9
+// us (2.8 for 64 x 64), and a segment's start and end, some 6. Tried: S's copy made column by column as U
+// is added (1 x 8192 x 32 heads on 8, backward: 346 us, 327 as it is); with one term of P and S, when it
+// took 69 us: P in columns of its own with w V in slots of 16 tokens, the next block's QK before this one's
+// intra (82 us); scores and outputs on two warpgroups, w V on one (82).
 //
 // No decay factor is ever above 1: every score is multiplied by its own l^{i-j}, from a table.
 #include <cuda.h>
@@ -73,7 +76,9 @@ template <int DK, int DV, bool STATES>
 struct Cfg {
     static constexpr uint32_t kQ = STATES ? 0 : kAtom * (DK / 64), kK = kAtom * (DK / 64), kV = kAtom * (DV / 64);
     static constexpr uint32_t kStage = kQ + kK + kV;
-    static constexpr uint32_t kS = DV * DK * 2;  // operand copy of S; staging of whole states
+    static constexpr uint32_t kSlot = DV * 128;  // operand copy of 32 columns of S
+    static constexpr uint32_t kS = STATES ? DV * DK * 2 : 2 * kSlot;   // two slots; staging of whole states
+    static_assert(kS >= (uint32_t)DV * DK * 2, "staging");
     static constexpr uint32_t kTail = 2560;      // the segments' powers and places, barriers
     static constexpr int kFit = (int)((kSmemMax - kS - kTail) / kStage);
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
@@ -133,6 +138,13 @@ __device__ __forceinline__ bool named_all(int id, int n, bool p)
                  : "r"((uint32_t)p), "r"(id), "r"(n)
                  : "memory");
     return r != 0;
+}
+// Two fp32 numbers as the sum of two pairs of bf16 each (what the first leaves is exact in fp32).
+__device__ __forceinline__ void split2(float2 t, uint32_t* hi, uint32_t* lo)
+{
+    *hi = pack_f2(t);
+    const float2 h = bf2_to_f2(*hi);
+    *lo = pack_bf16x2(t.x - h.x, t.y - h.y);
 }
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -237,10 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     // by stage, as the warp that waits may be more than a block behind
     auto o_staged = [&](int i) { return bar0 + 264 + 8 * i; };
     const uint32_t qk_done = bar0 + 192, p_ready = bar0 + 200, inter_done = bar0 + 208, inter_read = bar0 + 216,
-                   intra_done = bar0 + 224, o_free = bar0 + 232, u_done = bar0 + 240, u_free = bar0 + 248,
-                   s_ready = bar0 + 256;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 296);
-    static_assert(C::kOffBar + 300 <= C::kSmem, "barriers");
+                   intra_done = bar0 + 224, o_free = bar0 + 232, u_done = bar0 + 240, u_free = bar0 + 248;
+    // by slot of S's operand copy
+    auto s_ready = [&](int i) { return bar0 + 296 + 8 * i; };
+    auto s_free = [&](int i) { return bar0 + 312 + 8 * i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 328);
+    static_assert(C::kOffBar + 332 <= C::kSmem, "barriers");
     constexpr int kReaders = STATES ? 13 : 19;   // warps that read a work slot
 
     if (tid == 0) {
@@ -256,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(v_free(i), 1);
             mbar_init(w_full(i), 1);
             mbar_init(w_empty(i), kReaders);
+            mbar_init(s_ready(i), 128);
+            mbar_init(s_free(i), 1);
         }
         mbar_init(qk_done, 1);
         mbar_init(p_ready, 128);
@@ -265,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         mbar_init(o_free, 128);
         mbar_init(u_done, 1);
         mbar_init(u_free, 128);
-        mbar_init(s_ready, 128);
         fence_mbar_init();
     }
     if (warp == 17) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -425,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         const uint32_t in = left <= 0 ? 0u : (left < 32 ? (1u << left) - 1u : 0xffffffffu);
                         const uint32_t mask = rev ? from & in : to;
                         const float* t = tab + g;
-                        uint32_t p[16];
+                        uint32_t hi[16], lo[16];
                         tmem_wait_ld();
 #pragma unroll
                         for (int x = 0; x < 32; ++x) {
@@ -433,8 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                             v[x] = mask >> x & 1u ? y : 0.0f;
                         }
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) p[x] = pack_f2(mul2(splat2(ps), make_float2(v[2 * x], v[2 * x + 1])));
-                        tmem_st16(lanes + kColP + 16 * m, p);
+                        for (int x = 0; x < 16; ++x) split2(mul2(splat2(ps), make_float2(v[2 * x], v[2 * x + 1])), &hi[x], &lo[x]);
+                        tmem_st16(lanes + kColP + 32 * m, hi);
+                        tmem_st16(lanes + kColP + 32 * m + 16, lo);
                     }
                     if (n < kB) {     // P's zeros must not meet what rows behind the sequence hold
                         unsigned char* sv = smem + (size_t)st * C::kStage + C::kQ + C::kK + (n + r) * 128;
@@ -551,17 +567,28 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             if (!STATES) named_sync(4, 128);
             const float g = wk->log_l;
             for (int x0 = 0; x0 < nb; ++x0, ++i) {
-                if constexpr (!STATES) {     // S in bf16, the K-major operand of inter
-                    if (x0 > 0) wait(inter_done, i - 1);
-                    if (mine) {
+                if constexpr (!STATES) {     // the K-major operand of inter: rows of 32 columns of S, high terms, then low
 #pragma unroll
-                        for (int e = 0; e < DK; e += 8)
-                            *reinterpret_cast<uint4*>(smem + C::kOffS + (e / 64) * (DV * 128) + d * 128 + ((((e & 63) >> 3) ^ (d & 7)) << 4)) =
-                                make_uint4(pack_bf16x2(S[e], S[e + 1]), pack_bf16x2(S[e + 2], S[e + 3]),
-                                           pack_bf16x2(S[e + 4], S[e + 5]), pack_bf16x2(S[e + 6], S[e + 7]));
+                    for (int ch = 0; ch < DK / 32; ++ch) {
+                        const int use = i * (DK / 64) + (ch >> 1);           // of slot ch & 1
+                        if (use > 0) wait(s_free(ch & 1), use - 1);
+                        if (mine) {
+                            unsigned char* row = smem + C::kOffS + (ch & 1) * C::kSlot + d * 128;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const int e = 32 * ch + 8 * y + 2 * z;
+                                    split2(make_float2(S[e], S[e + 1]), &hi[z], &lo[z]);
+                                }
+                                *reinterpret_cast<uint4*>(row + ((y ^ (d & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                *reinterpret_cast<uint4*>(row + (((4 + y) ^ (d & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            }
+                        }
+                        fence_async_smem();
+                        mbar_arrive_local(s_ready(ch & 1));
                     }
-                    fence_async_smem();
-                    mbar_arrive_local(s_ready);
                 }
                 const LinearDecay dec(g * (float)tokens(nall, block(rev, nb, x0)));
                 const float2 f2 = splat2(dec.f), keep2 = splat2(dec.slow ? 1.0f : 0.0f);
@@ -718,9 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 close(k);
                 for (int x0 = 0; x0 < nb; ++x0, ++i) {
                     const int st = i % C::kStages;
-                    const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK, ss = sb + C::kOffS;
+                    const uint32_t sq = sb + (uint32_t)st * C::kStage, sk = sq + C::kQ, sv = sk + C::kK;
                     // descriptors count addresses in 16 bytes
-                    const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), sd = sdesc_sw128(ss), vmn = sdesc_sw128_mn(sv);
+                    const uint64_t qd = sdesc_sw128(sq), kd = sdesc_sw128(sk), vmn = sdesc_sw128_mn(sv);
                     wait(kv_full(st), i / C::kStages);
                     wait(q_full(st), i / C::kStages);
                     fence_after_sync();
@@ -733,24 +760,34 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         mma_commit(qk_done);
                     }
                     __syncwarp();
-                    wait(s_ready, i);
                     if (i > 0) wait(o_free, i - 1);
-                    fence_after_sync();
-                    if (leader) {
 #pragma unroll
-                        for (int x = 0; x < DK / 16; ++x)
-                            mma_bf16(tmem + kColO, qd + (((x >> 2) * kAtom + (x & 3) * 32) >> 4),
-                                     sd + (((x >> 2) * (DV * 128) + (x & 3) * 32) >> 4), idesc_bf16(128, DV, 0, 0), x > 0);
-                        mma_commit(inter_done);
+                    for (int ch = 0; ch < DK / 32; ++ch) {
+                        wait(s_ready(ch & 1), i * (DK / 64) + (ch >> 1));
+                        fence_after_sync();
+                        if (leader) {
+                            const uint64_t sd = sdesc_sw128(sb + C::kOffS + (ch & 1) * C::kSlot);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {                    // two steps of 16 columns, high terms and low
+                                const int x = 2 * ch + (y & 1);
+                                mma_bf16(tmem + kColO, qd + (((x >> 2) * kAtom + (x & 3) * 32) >> 4), sd + (y * 32 >> 4),
+                                         idesc_bf16(128, DV, 0, 0), ch + y > 0);
+                            }
+                            mma_commit(s_free(ch & 1));
+                            if (ch == DK / 32 - 1) mma_commit(inter_done);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     wait(p_ready, i);
                     wait(inter_read, i);
                     fence_after_sync();
                     if (leader) {
 #pragma unroll
                         for (int x = 0; x < kB / 16; ++x)
-                            mma_bf16_ts(tmem + kColO, tmem + kColP + x * 8, vmn + (uint64_t)(x * 2048 >> 4), idesc_bf16(128, DV, 0, 1), 1);
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+                                mma_bf16_ts(tmem + kColO, tmem + kColP + (x >> 1) * 32 + t * 16 + (x & 1) * 8, vmn + (uint64_t)(x * 2048 >> 4),
+                                            idesc_bf16(128, DV, 0, 1), 1);
                         mma_commit(intra_done);
                         if (a.early) mma_commit(kv_empty(st));
                     }
