@@ -759,7 +759,8 @@ ssd_status ssd_mixer_layer_norm_backward(int64_t rows, int32_t groups, int32_t w
     p.x = x; p.x_ld = x_ld; p.dy = dy; p.dy_ld = dy_ld; p.weight = weight;
     p.y = dx; p.y_ld = dx_ld;
     p.mean = const_cast<float*>(mean); p.rstd = const_cast<float*>(rstd);
-    p.dweight = dweight; p.dbias = dbias; p.part = (float*)workspace;
+    p.dweight = dweight; p.dbias = dbias;
+    p.part = dweight || dbias ? (float*)workspace : nullptr;   // checked above only where it is wanted
     return ssd::launch_layer_norm_backward(p, parts, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

@@ -17,7 +17,7 @@ struct LayerNorm {
     int64_t y_ld;
     float *mean, *rstd;             // [rows][groups]; written forwards (nullptr: not wanted), read backwards
     float *dweight, *dbias;         // [groups * width], or nullptr: not wanted
-    float* part;                    // workspace: [layer_norm_parts][2][groups * width]
+    float* part;                    // workspace: [layer_norm_parts][2][groups * width]; nullptr: no parameter gradients wanted
 
     SSD_HD int64_t channels() const { return (int64_t)groups * width; }
 };
