@@ -331,7 +331,10 @@ __device__ bool nth_long(const LinearCall& c, int n, int64_t* seq)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int64_t base = 0; base < c.b && n >= 0; base += 256) {
         const int64_t i = base + threadIdx.x;
-        const bool is = i < c.b && (int64_t)c.cu_seqlens[i + 1] - c.cu_seqlens[i] > c.seg_tokens;
+        LinearItem it;
+        it.nseg = 0;
+        if (i < c.b) linear_packed_item(c, i, 0, &it);     // of its rows, not its offsets: those may lie outside 0 .. T
+        const bool is = it.nseg > 1;
         const unsigned all = __ballot_sync(0xffffffffu, is);
         if (lane == 0) longs[warp] = __popc(all);
         __syncthreads();
