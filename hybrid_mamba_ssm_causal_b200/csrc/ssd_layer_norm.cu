@@ -404,9 +404,13 @@ __global__ void __launch_bounds__(TEAM ? 128 : (NV > 4 ? 512 : 1024)) layer_norm
     }
 }
 
-// dx = rs dy w + (A x + B), A = -rs rs mean(dh xh), B = -rs mean(dh) - m A: three operations an element.
-// 16384 x 8192 bf16: 171 us, 4.7 TB/s, bound by issue slots (70 %); 32768 x 64 groups of 128 274 us, 5.9;
-// 2048 x 2688 fp32 some 14 us: 14 rows a block, each a barrier and two sums after the other.
+// dx = rs dy w + (A xh + B), A = -rs mean(dh xh), B = -rs mean(dh): three operations an element. xh = (x - m) rs
+// takes the difference first: of close numbers it is exact, where the rounding of m rs in x rs - m rs is the
+// same over a whole row (dweight of rows at 1000 spreads from zero was off by 2e-5 of its size, now 4e-8). Block
+// teams keep xh in registers for dx where there is room (16384 x 8192 bf16: 177 us, 210 without); lane teams
+// take x - m again (32768 x 64 groups of 128: 280 us, 296 with it kept).
+// 16384 x 8192 bf16: 177 us, 4.6 TB/s: one block to an SM, whose rows follow one another through a barrier and
+// two sums; 32768 x 64 groups of 128 280 us, 5.8; 2048 x 2688 fp32 some 14 us: 14 rows a block in the same way.
 template <typename T, int VB, int NV, int TEAM>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) layer_norm_grad_kernel(const LayerNorm p)
 {
@@ -432,36 +436,39 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) layer_norm_grad_kernel(c
     }
     T* dx = (T*)p.y + it.row * p.y_ld + it.col(0);
     for (int k = 0; it.row < p.rows; it.row += it.stride, k ^= 1) {
-        const float rs = r_next, c = -m_next * rs, m = m_next;
+        const float rs = r_next, m = m_next;
         if (it.row + it.stride < p.rows) {
             m_next = *(mp += sstep);
             r_next = *(rp += sstep);
         }
         V v[2][NV];
         it.take(p, v);
-        float s1 = 0.0f, s2 = 0.0f;
+        float s1 = 0.0f, s2 = 0.0f, xhs[NV][V::kN];
+        constexpr bool kKeep = TEAM == 0 && (NV == 1 || sizeof(T) == 4);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (it.in(i)) {
                 if (NV > 1) load_params<V::kN>(p.weight, it.col(i), 1.0f, w);
 #pragma unroll
                 for (int e = 0; e < V::kN; ++e) {
-                    const float d = v[1][i].at(e), xh = fmaf(v[0][i].at(e), rs, c), dh = d * w[e];
+                    const float d = v[1][i].at(e), xh = (v[0][i].at(e) - m) * rs, dh = d * w[e];
                     dw[i][e] = fmaf(d, xh, dw[i][e]);
                     db[i][e] += d;
                     s1 += dh;
                     s2 = fmaf(dh, xh, s2);
+                    if (kKeep) xhs[i][e] = xh;
                 }
             }
         const float2 s = team_sum2<TEAM>(s1, s2, red[k]);
-        const float A = -rs * rs * (s.y * inv), B = fmaf(-m, A, -rs * (s.x * inv));
+        const float A = -rs * (s.y * inv), B = -rs * (s.x * inv);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (it.in(i)) {
                 if (NV > 1) load_params<V::kN>(p.weight, it.col(i), 1.0f, w);
                 float f[V::kN];
 #pragma unroll
-                for (int e = 0; e < V::kN; ++e) f[e] = fmaf(v[1][i].at(e), rs * w[e], fmaf(v[0][i].at(e), A, B));
+                for (int e = 0; e < V::kN; ++e)
+                    f[e] = fmaf(v[1][i].at(e), rs * w[e], kKeep ? fmaf(xhs[i][e], A, B) : fmaf(v[0][i].at(e) - m, A * rs, B));
                 V o;
                 o.set(f);
                 o.store(dx + i * it.step * V::kN);
