@@ -106,8 +106,13 @@ int64_t linear_segment_tokens(bool tc, int64_t b, int64_t L, int64_t T, bool pac
 
 #ifdef __CUDACC__
 
-// lambda = exp(log_decay): -inf (no memory) is taken as exp(-1e4) = 0 so that 0 * log_decay is 0.
-__device__ __forceinline__ float linear_log_decay(const float* log_decay, int h) { return fmaxf(log_decay[h], -1e4f); }
+// lambda = exp(log_decay): -inf (no memory) is taken as exp(-1e4) = 0 so that 0 * log_decay is 0. NaN stays
+// NaN (fmaxf would drop it).
+__device__ __forceinline__ float linear_log_decay(const float* log_decay, int h)
+{
+    const float g = log_decay[h];
+    return g < -1e4f ? -1e4f : g;
+}
 
 // One step of a decayed sum, S <- l S + add. A slow decay (l > 1/2) is taken as S + (l - 1) S: l
 // itself rounded to fp32 would be off by up to 2^-25 in every step, the same way each time, 3e-3

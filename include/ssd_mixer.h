@@ -431,7 +431,7 @@ SSD_API ssd_status ssd_mixer_backward(const ssd_dims* dims,
  *   S_t = l S_{t-1} + v_t (outer) k_t,   o_t = scale S_t q_t.
  * The state S is fp32 [H][dv][dk], dk contiguous (the layout of the SSM state). log_decay [H] fp32,
  * at most 0, is a constant: no gradient with respect to it is computed. -inf keeps the current
- * token alone, 0 forgets nothing.
+ * token alone, 0 forgets nothing, NaN makes its head's results NaN.
  *
  * Shared by the linear_* calls: row layouts as above, each row's heads side by side (q [..][H][dk],
  * k [..][G][dk], v [..][G][dv], o [..][H][dv]), strides of at least that many elements; pointers
