@@ -74,3 +74,26 @@ def test_more_sequences_than_one_block_counts(kind):
         offsets.append(offsets[-1] + n)
     d = check_packed(kind, offsets, offsets[-1] + 5, [i % 4 != 2 for i in range(300)], seed=4)
     assert segment_tokens_at_most(d) < sorted(long)[1]       # one of them behind the first 256
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("poison", [None, 1, 2])
+@pytest.mark.parametrize("flip", [0, 1])
+def test_several_sequences_cut_at_once(kind, poison, flip):
+    """Three sequences in segments among short, empty and single-token ones, continuing from their slots and not,
+    all compared, or beside one of NaN (a short one, the longest)."""
+    lens = [1700, 3, 2600, 0, 1025, 1] if kind[0] == "bf16" else [333, 3, 500, 0, 257, 1]
+    offsets = [4]
+    for n in lens:
+        offsets.append(offsets[-1] + n)
+    d = check_packed(kind, offsets, offsets[-1] + 7, [(i // 2 + flip) % 2 for i in range(6)], seed=5 + flip, poison=poison)
+    assert segment_tokens_at_most(d) < sorted(lens)[-2]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("has", [0, 1])
+def test_one_long_sequence(kind, has):
+    """A packed call of one sequence is cut as a single row is."""
+    n = 4000 if kind[0] == "bf16" else 700
+    d = check_packed(kind, [3, 3 + n], n + 20, [has], seed=6)
+    assert segment_tokens_at_most(d) < n
