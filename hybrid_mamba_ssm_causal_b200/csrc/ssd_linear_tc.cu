@@ -34,7 +34,7 @@
 // unrolled by four: 106 us where 72 are). Nothing may spill: beside 227 KB of shared memory the L1 has some
 // 16 KB left, and a reload waits behind the tiles.
 //
-// Measured: 1 x 2048 tokens x 148 heads of 128, a row per SM, 82 us (4.0 TB/s of operands): 5.1 us a block,
+// Measured: 1 x 2048 tokens x 148 heads of 128, a row per SM, 84 us (3.9 TB/s of operands): 5.2 us a block,
 // of which 2.3 are matrix instructions and 2.5 HBM. With few rows the chain of one block bounds it, 3.8-3.9
 // us (2.8 for 64 x 64), and a segment's start and end, some 6. Tried: S's copy made column by column as U
 // is added (1 x 8192 x 32 heads on 8, backward: 346 us, 327 as it is); with one term of P and S, when it
@@ -42,6 +42,11 @@
 // intra (82 us); scores and outputs on two warpgroups, w V on one (82).
 //
 // No decay factor is ever above 1: every score is multiplied by its own l^{i-j}, from a table.
+//
+// Scores of tokens that do not see one another are selected away, whatever q and k hold; but their zeros meet v in
+// P V. w V's warps, which look at every value of v, tell the outputs' of a block with values that are not finite,
+// and those keep them out of the product (one packed product for each pair of values and a barrier a block: 82 ->
+// 84 us in the case above, 64 x 64 57 -> 61).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -79,7 +84,7 @@ struct Cfg {
     static constexpr uint32_t kSlot = DV * 128;  // operand copy of 32 columns of S
     static constexpr uint32_t kS = STATES ? DV * DK * 2 : 2 * kSlot;   // two slots; staging of whole states
     static_assert(kS >= (uint32_t)DV * DK * 2, "staging");
-    static constexpr uint32_t kTail = 2560;      // the segments' powers and places, barriers
+    static constexpr uint32_t kTail = 2688;      // the segments' powers and places, barriers, what is not finite
     static constexpr int kFit = (int)((kSmemMax - kS - kTail) / kStage);
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static_assert(kStages >= 2, "two stages");
@@ -253,16 +258,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     // by slot of S's operand copy
     auto s_ready = [&](int i) { return bar0 + 296 + 8 * i; };
     auto s_free = [&](int i) { return bar0 + 312 + 8 * i; };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 328);
-    static_assert(C::kOffBar + 332 <= C::kSmem, "barriers");
+    // by stage: w V's warps may be some blocks ahead of the outputs
+    auto v_seen = [&](int i) { return bar0 + 328 + 8 * i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 360);
+    // bad[i & 7] = i + 1: v of block i has values that are not finite. They are at most kStages + 1 blocks ahead of
+    // its reader. from[d]: where in the block column d's first lies.
+    int* bad = reinterpret_cast<int*>(smem + C::kOffBar + 368);
+    unsigned char* from = smem + C::kOffBar + 400;
+    const uint32_t from_full = bar0 + 528, from_read = bar0 + 536;
+    static_assert(C::kOffBar + 544 <= C::kSmem && C::kStages + 1 < 8, "barriers");
     constexpr int kReaders = STATES ? 13 : 19;   // warps that read a work slot
 
     if (tid == 0) {
+        for (int i = 0; i < 8; ++i) bad[i] = 0;
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
             mbar_init(kv_full(i), 1);
             mbar_init(o_staged(i), 128);
+            mbar_init(v_seen(i), 256);
             mbar_init(kv_empty(i), STATES ? 1 : 2);   // U's MMAs, and intra's or the stores
         }
         for (int i = 0; i < 2; ++i) {
@@ -273,6 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(s_ready(i), 128);
             mbar_init(s_free(i), 1);
         }
+        mbar_init(from_full, 128);
+        mbar_init(from_read, 128);
         mbar_init(qk_done, 1);
         mbar_init(p_ready, 128);
         mbar_init(inter_done, 1);
@@ -355,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     fence_async_smem();
                 }
                 if (n < kB) named_sync(3, 256);
+                float2 seen = splat2(0.0f);          // NaN once one of v's values is infinite or NaN
 #pragma unroll 1
                 for (int u = first; u < kB / kSub; u += 2) {
                     const int kk = i * (kB / kSub) + u;
@@ -385,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 #pragma unroll
                                 for (int y = 0; y < 2; ++y) {
                                     const float2 v = bf2_to_f2(raw[y][x]);
+                                    if (!STATES) seen = fma2(v, splat2(0.0f), seen);
                                     float2 t = mul2(v, w[x]);
                                     const uint32_t h0 = pack_f2(t);
                                     float2 b0 = bf2_to_f2(h0);
@@ -405,6 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     fence_before_sync();
                     mbar_arrive_local(v_ready(kk & 1));
                 }
+                if (!STATES) {
+                    if (!(seen.x == 0.0f && seen.y == 0.0f)) bad[i & 7] = i + 1;
+                    mbar_arrive_local(v_seen(st));
+                }
             }
             close(k);
         }
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if constexpr (!STATES) {
             const int r = tid;                                     // row i of the block = TMEM lane
             const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-            int i = 0;
+            int i = 0, rare = 0;                                   // blocks, and those with values that are not finite
             for (int k = 0;; ++k) {
                 const Work* wk = open(k, 1, 128);
                 if (!wk) break;
@@ -481,6 +503,40 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         tmem_st32(lanes + kColO + x, v);
                     }
                     tmem_wait_st();
+                    wait(v_seen(st), i / C::kStages);
+                    if (__all_sync(0xffffffffu, bad[i & 7] == i + 1)) {
+                        // Zeros of P must not meet what is not finite: its place in the V tile becomes zero (w V has read
+                        // it), and its column of o NaN from its token on, in scan order, for intra to add to.
+                        if (rare > 0) wait(from_read, rare - 1);
+                        if (r < DV) {
+                            unsigned char* sv = smem + (size_t)st * C::kStage + C::kQ + C::kK + (r >> 6) * kAtom + (r & 7) * 2;
+                            int at = rev ? 0 : 255;
+#pragma unroll 1
+                            for (int j = 0; j < n; ++j) {
+                                unsigned short* v = reinterpret_cast<unsigned short*>(sv + j * 128 + ((((r & 63) >> 3) ^ (j & 7)) << 4));
+                                if ((*v & 0x7f80) != 0x7f80) continue;
+                                *v = 0;
+                                at = rev ? j + 1 : min(at, j);
+                            }
+                            from[r] = (unsigned char)at;
+                        }
+                        fence_async_smem();
+                        mbar_arrive_local(from_full);
+                        wait(from_full, rare);
+#pragma unroll 1
+                        for (int x = 0; x < DV; x += 16) {
+                            float v[16];
+                            tmem_ld16(lanes + kColO + x, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int y = 0; y < 16; ++y)
+                                if (rev ? r < from[x + y] : r >= from[x + y]) v[y] = __int_as_float(0x7fffffff);
+                            tmem_st16(lanes + kColO + x, reinterpret_cast<const uint32_t*>(v));
+                        }
+                        tmem_wait_st();
+                        mbar_arrive_local(from_read);
+                        ++rare;
+                    }
                     fence_before_sync();
                     mbar_arrive_local(inter_read);
                     wait(intra_done, i);

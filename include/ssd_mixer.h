@@ -439,7 +439,9 @@ SSD_API ssd_status ssd_mixer_backward(const ssd_dims* dims,
  * the gradients must not overlap the inputs or one another. dk and dv: 16, 32, 64 or 128, in any
  * pairing. Arithmetic is fp32; bf16 calls with dk and dv of 64 or 128 run their products on the
  * tensor cores with fp32 accumulation, the decayed scores and the state's operand copy taken with 16
- * bits, the state itself carried in fp32 and added to from products of 24-bit operands. */
+ * bits, the state itself carried in fp32 and added to from products of 24-bit operands. A value that
+ * is not finite reaches the tokens and columns that its formula names and no others; there an infinity
+ * may come out as NaN. */
 typedef struct ssd_linear_dims {
     int64_t batch;    /* sequences */
     int64_t seqlen;   /* tokens per row (packed call: token rows in all; decode: must be 1) */
