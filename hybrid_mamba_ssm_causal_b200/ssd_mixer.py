@@ -675,7 +675,8 @@ class _On:
         if stream is None:
             return _raw_stream(dev.index)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+            handle = _stream(stream)     # 0, the default stream, is no external one: ExternalStream(0) is some new stream
+            stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
         if stream.device != dev:
             self.__exit__(None, None, None)
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
