@@ -670,16 +670,16 @@ class _On:
         dev, stream = self.dev, self.stream
         if stream is None and torch.cuda.current_device() == dev.index:
             return _raw_stream(dev.index)
-        self.ctx = [torch.cuda.device(dev)]
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                handle = _stream(stream)     # 0, the default stream, is no external one: ExternalStream(0) is some new stream
+                stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.ctx = [torch.cuda.device(dev)]      # entered when nothing can refuse any more
         self.ctx[0].__enter__()
         if stream is None:
             return _raw_stream(dev.index)
-        if not isinstance(stream, torch.cuda.Stream):
-            handle = _stream(stream)     # 0, the default stream, is no external one: ExternalStream(0) is some new stream
-            stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
-        if stream.device != dev:
-            self.__exit__(None, None, None)
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
         self.ctx.append(torch.cuda.stream(stream))
         self.ctx[1].__enter__()
         return stream.cuda_stream
