@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(32 * (DV / SimtShape<DK>::kWarpRows > 0 ? DV /
     const int h = blockIdx.x % c.H;
     const int64_t item = blockIdx.x / c.H;
     LinearItem it;
-    if (!linear_item(c, item, &it)) return;
+    if (!linear_item(c, item, &it) || !SSD_IN_BOUNDS(c.status, linear_in_bounds(c, it) && item < c.items)) return;
     // segments in scan order; the state-only pass covers all but the last of a row
     const bool last = s.reverse ? it.seg == 0 : it.seg == it.nseg - 1;
     if (state_only && last) return;
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(256) linear_pass_kernel(const LinearCall c, co
     }
     __syncthreads();
     const int64_t nseg = first.nseg;
+    if (nseg > 0 && !SSD_IN_BOUNDS(c.status, linear_in_bounds(c, first) && item0 >= 0 && item0 + nseg <= c.items)) return;
     // pieces before the scan's last segment, whose entering state ends the walk
     const int64_t before = s.reverse ? nseg - c.sub : (nseg - 1) / c.sub * c.sub;
     if (before < 1) return;

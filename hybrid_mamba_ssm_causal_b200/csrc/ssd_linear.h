@@ -71,7 +71,21 @@ struct LinearCall {
     int* counts;
 };
 
-inline LinearCall linear_pieces(const LinearCall& c)
+// Who clears the status word. In the bounds-checked build blocks may set it from their start on, before block
+// 0 of the same kernel would clear it.
+inline cudaError_t set_clear_status(LinearCall* c, cudaStream_t st)
+{
+#ifdef SSD_DEBUG_BOUNDS
+    c->clear_status = false;
+    return clear_device_status(c->status, st);
+#else
+    (void)st;
+    c->clear_status = true;
+    return cudaSuccess;
+#endif
+}
+
+SSD_HD inline LinearCall linear_pieces(const LinearCall& c)
 {
     LinearCall f = c;
     if (c.sub > 1) {
@@ -173,6 +187,11 @@ __device__ __forceinline__ bool linear_item(const LinearCall& c, int64_t item, L
     const int64_t left = c.L - it->seg * c.seg_tokens;
     it->n = left < c.seg_tokens ? left : c.seg_tokens;
     return it->seg < it->nseg;
+}
+// Its rows and its slot lie inside the call's.
+__device__ __forceinline__ bool linear_in_bounds(const LinearCall& c, const LinearItem& it)
+{
+    return it.n >= 0 && it.row0 >= 0 && it.row0 + it.n <= c.T && it.slot >= 0 && it.slot < c.nslots;
 }
 // Whether the sequence continues from the state in its slot.
 __device__ __forceinline__ bool linear_has_init(const LinearCall& c, const LinearScan& s, int64_t seq)

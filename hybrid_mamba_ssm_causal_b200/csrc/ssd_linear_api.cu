@@ -175,7 +175,7 @@ ssd_status ssd_mixer_linear_prefill(const ssd_linear_dims* d, const void* q, int
     c.status = (int*)workspace;
     cudaStream_t st = (cudaStream_t)stream;
     c.taken = c.status + 1;
-    c.clear_status = true;
+    if (ssd::set_clear_status(&c, st) != cudaSuccess) return SSD_ERR_CUDA;
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, init_state, o, o_ld, final_state, (char*)workspace, w);
     if (d->seqlen <= ssd::kLinearShort)
         return ssd::launch_linear_short(c, s, false, false, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
@@ -217,7 +217,7 @@ ssd_status ssd_mixer_linear_prefill_varlen(const ssd_linear_dims* d, const int32
     c.status = (int*)workspace;
     cudaStream_t st = (cudaStream_t)stream;
     c.taken = c.status + 1;
-    c.clear_status = true;
+    if (ssd::set_clear_status(&c, st) != cudaSuccess) return SSD_ERR_CUDA;
     const ssd::LinearScan s = prefill_scan(d, q, q_ld, k, k_ld, v, v_ld, state, o, o_ld, state, (char*)workspace, w);
     return run(c, &s, 1, st);
 }
@@ -315,7 +315,7 @@ ssd_status ssd_mixer_linear_backward(const ssd_linear_dims* d, const void* q, in
     }
     for (int i = 0; i < 3; ++i) s[i].seg_states = (float*)(ws + w.seg + i * w.seg_each);
     c.taken = c.status + 1;
-    c.clear_status = true;
+    if (ssd::set_clear_status(&c, st) != cudaSuccess) return SSD_ERR_CUDA;
     const ssd_status rs = run(c, s, 3, st);
     if (rs != SSD_OK || r == 1) return rs;
     if (ssd::launch_linear_group_sum((const float*)(ws + w.part_k), dk, dk_ld, c.T, d->ngroups, r, d->dk, d->act, st) != cudaSuccess ||

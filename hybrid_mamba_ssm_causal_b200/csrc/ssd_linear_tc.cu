@@ -719,7 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     }
                     break;
                 }
-                const bool end = w >= total;
+                // segment states: pieces of this launch, or of the states' pass before it
+                const bool end = w >= total ||
+                                 !SSD_IN_BOUNDS(c.status, linear_in_bounds(c, it) && (it.nseg == 1 || item < (STATES ? c : linear_pieces(c)).items));
                 if (k >= 2) wait(w_empty(k & 1), (k >> 1) - 1);
                 ok = __all_sync(0xffffffffu, ok);
                 Work* wk = works + (k & 1);
