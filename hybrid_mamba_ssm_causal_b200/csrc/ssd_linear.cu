@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kListThreads) linear_list_kernel(const LinearC
 // Up to kLinearShort tokens of each row, token by token: the fp32 state is read once and written once,
 // which for a few tokens is nearly all of the bytes. Lanes along DK (a float4 each), kRif state rows in
 // flight per lane, so a CTA's whole part of the state is on its way before the first product.
-// 256 sequences of 128 heads of 128 x 64: 323 us a step, 6.7 TB/s; one token of 32 heads of 128: 2.7 us.
+// 256 sequences of 128 heads of 128 x 64: 324 us a step, 6.7 TB/s; one token of 32 heads of 128: 2.6 us.
 constexpr int kShortThreads = 128, kRif = 8;
 
 struct LinearShort {

@@ -109,7 +109,7 @@ cudaError_t launch_linear_group_sum(const float* in, void* out, int64_t ld, int6
                                     cudaStream_t st);
 // Forward scans of rows of at most kLinearShort tokens (one: of exactly one token each) on CUDA cores;
 // in a packed call, of those rows alone. Rows of 8 tokens (9: the tensor-core scan's whole block): 64
-// sequences of 32 heads of 128 98 us (109), of 64 24 (72); 1 sequence of 8 heads of 64 6.2 (8.4).
+// sequences of 32 heads of 128 99 us (123), of 64 23 (80); 1 sequence of 8 heads of 64 6.0 (8.7).
 constexpr int kLinearShort = 8;
 cudaError_t launch_linear_list(const LinearCall& c, cudaStream_t st);
 // `follows`: it comes after another kernel of the call.

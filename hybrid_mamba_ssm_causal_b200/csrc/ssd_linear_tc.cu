@@ -36,7 +36,7 @@
 //
 // Measured: 1 x 2048 tokens x 148 heads of 128, a row per SM, 84 us (3.9 TB/s of operands): 5.2 us a block,
 // of which 2.3 are matrix instructions and 2.5 HBM. With few rows the chain of one block bounds it, 3.8-3.9
-// us (2.8 for 64 x 64), and a segment's start and end, some 6. Tried: S's copy made column by column as U
+// us (2.9 for 64 x 64), and a segment's start and end, some 6. Tried: S's copy made column by column as U
 // is added (1 x 8192 x 32 heads on 8, backward: 346 us, 327 as it is); with one term of P and S, when it
 // took 69 us: P in columns of its own with w V in slots of 16 tokens, the next block's QK before this one's
 // intra (82 us); scores and outputs on two warpgroups, w V on one (82).

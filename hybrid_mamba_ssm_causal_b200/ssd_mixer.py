@@ -21,7 +21,9 @@ Linear attention with a decay per head (:class:`LinearDims`, :func:`linear_prefi
 :func:`linear_prefill_varlen`, :func:`linear_decode_step`, :func:`linear_backward`) and the
 grouped layer norm (:func:`layer_norm`, :func:`layer_norm_backward`) check every tensor's type,
 shape and device, run on the device of their inputs whichever is current, and allocate what is
-not given. Unless ``stream`` is given, they run on that device's current stream.
+not given. Unless ``stream`` (a torch stream or a handle) is given, they run on that device's
+current stream. A call's status word (:func:`ssd_mixer_workspace_status`) can be read where
+``workspace`` was given.
 """
 from __future__ import annotations
 
