@@ -588,6 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         const bool mine = d < DV;
         const int64_t hs = (int64_t)DK * DV;
         unsigned char* buf = smem + C::kOffS + (size_t)(warp - 4) * 32 * (DK * 2);   // this warp's rows of the operand copy's room
+        // The operand copies of the first n blocks have been read. (Not by inter_done: its last but one completion
+        // is not waited for here.)
+        auto copy_read = [&](int n) {
+            if (n > 0)
+                for (int x = 0; x < 2; ++x) wait(s_free(x), n * (DK / 64) - 1);
+        };
         int i = 0;
         for (int k = 0;; ++k) {
             const Work* wk = open(k, 4, 128);
@@ -595,8 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             const LinearScan& s = a.s[wk->scan];
             const int flags = wk->flags, nall = wk->n, nb = (nall + kB - 1) / kB;
             const bool rev = s.reverse;
-            // the operand copy of the segment before has been read
-            if (!STATES && i > 0) wait(inter_done, i - 1);
+            if (!STATES) copy_read(i);
             float S[DK];
 #pragma unroll
             for (int e = 0; e < DK; ++e) S[e] = 0.0f;
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             if (STATES) out = s.seg_states + ((int64_t)wk->item * c.H + wk->head) * hs;
             else if ((flags & kFinal) && s.final_state) out = s.final_state + ((int64_t)wk->slot * c.H + wk->head) * hs;
             if (out) {
-                if (!STATES && nb > 0) wait(inter_done, i - 1);
+                if (!STATES) copy_read(i);
                 if (mine) store_state<DK>(out + (int64_t)(d - lane) * DK, buf, lane, S);
             }
             close(k);
